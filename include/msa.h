@@ -25,8 +25,10 @@
  * of the selected documents' recurrent states that the linear (DGA) layers
  * take as their initial state (msa_state_gather_sum, from the "MSA x Qwen3.5"
  * model card) and the gated delta rule that starts from it
- * (msa_gated_delta_rule), and a routing entry point that allocates nothing
- * (msa_route_topk_noalloc).
+ * (msa_gated_delta_rule), a routing entry point that allocates nothing
+ * (msa_route_topk_noalloc), and for serving the rotary positions (msa_rope),
+ * a paged cache of the local keys and values (msa_paged_append) and the
+ * attention of new tokens over it (msa_paged_attn).
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -506,6 +508,150 @@ msa_status msa_state_gather_sum(msa_dtype dt, const void* states, int64_t D, int
 msa_status msa_gated_delta_rule(msa_dtype dt, const void* q, const void* k, const void* v, const float* g,
                                 const float* beta, int64_t B, int T, int Hk, int Hv, int dk, int dv,
                                 const float* h0, float scale, void* o, float* hT, msa_stream_t stream);
+
+/* ========================================================================
+ * Rotary positions and the paged cache of the local keys and values.  The
+ * memory path above takes the local K / V as dense rows, already rotated by
+ * the caller.  These entry points hold what a serving loop has around it:
+ * the rotation itself, a cache of pages that requests of different lengths
+ * share, and the layer's attention with its local part read from that cache.
+ * ====================================================================== */
+
+/* Pairs of a rotation over the first rd dimensions of a head: (x_i, x_{i + rd/2})
+ * or (x_{2i}, x_{2i+1}), 0 <= i < rd/2; the dimensions past rd are not rotated. */
+typedef enum { MSA_ROPE_HALF = 0, MSA_ROPE_INTERLEAVED = 1 } msa_rope_layout;
+
+/* How msa_rope_table_scaled_host stretches the angles for longer contexts. */
+enum {
+  MSA_ROPE_SCALE_NONE = 0,   /* theta^(-2i/rd), as msa_rope_table_host */
+  MSA_ROPE_SCALE_LINEAR = 1, /* every frequency divided by factor (position interpolation) */
+  MSA_ROPE_SCALE_NTK = 2,    /* theta * factor^(rd / (rd - 2)) in the place of theta */
+  MSA_ROPE_SCALE_YARN = 3,   /* by parts, with a magnitude ("YaRN", Peng et al. 2023) */
+  MSA_ROPE_SCALE_BANDS = 4,  /* by each frequency's turns over the original length */
+};
+
+/* ------------------------------------------------------------------------
+ * RoPE table (host) with scaled angles: host_out[max_len][rd/2][2] = m (cos,
+ * sin) of p * f_i, computed in fp64 and stored as fp32, where f_i comes from
+ * f = theta^(-2i/rd):
+ *   LINEAR  f / factor
+ *   NTK     (theta factor^(rd/(rd-2)))^(-2i/rd)
+ *   YARN    f (1 - t) + f / factor * t, with t = clamp((i - a) / (b - a), 0, 1),
+ *           a = max(floor(x(hi)), 0), b = min(ceil(x(lo)), rd - 1),
+ *           x(r) = rd ln(orig_len / (2 pi r)) / (2 ln theta) (the dimension that
+ *           turns r times over orig_len; b = a + 0.001 where b <= a), and the
+ *           magnitude m = 0.1 ln(factor) + 1 (else m = 1)
+ *   BANDS   f s + f / factor * (1 - s), s = clamp((n - lo) / (hi - lo), 0, 1) for
+ *           n = orig_len f / (2 pi) turns over the original length
+ * orig_len, lo and hi are read by YARN and BANDS only, factor by all but NONE.
+ * Errors: MSA_ERR_INVALID_ARG for a NULL host_out, rd odd or < 2, max_len < 1,
+ * theta <= 0, an unknown method, factor < 1 or not finite, and for YARN and BANDS
+ * orig_len <= 0 or not 0 < lo < hi; theta <= 1 with YARN; rd < 4 with NTK.
+ * ---------------------------------------------------------------------- */
+msa_status msa_rope_table_scaled_host(int method, double theta, int rd, int max_len, double factor, double orig_len,
+                                      double lo, double hi, float* host_out);
+
+/* ------------------------------------------------------------------------
+ * Rotary positions.  With (c, s) = rope_cs[pos[n]][i] and (a, b) pair i of head
+ * h of token n:
+ *   out pair = (a c - b s, a s + b c);   out[rd..d) = x[rd..d)
+ * in fp32, rounded once.  msa_rope_backward is the exact adjoint, for the
+ * gradient dx of an upstream gradient dout: (a c + b s, b c - a s).
+ *   x, out   [N, H, d] dtype dt, d contiguous, token and head strides in
+ *            elements (multiples of 16 bytes), so the heads of a fused
+ *            projection can be read in place.  out's elements must not overlap;
+ *            out may be x itself with the same strides, and must not overlap x
+ *            otherwise.
+ *   pos      int32 [N];  rope_cs fp32 [max_len, rd/2, 2] (msa_rope_table_host or
+ *            msa_rope_table_scaled_host for rd dimensions).
+ * Supported: rd and d multiples of 16, rd <= d <= 1024.  Device flags:
+ * MSA_FLAG_INDEX_OOB for a position outside [0, max_len) (that token's rows of
+ * out are left as they were).
+ * ---------------------------------------------------------------------- */
+msa_status msa_rope(msa_dtype dt, const void* x, int64_t x_tok_stride, int64_t x_head_stride, int64_t N, int H, int d,
+                    const int32_t* pos, const float* rope_cs, int max_len, int rd, msa_rope_layout layout, void* out,
+                    int64_t out_tok_stride, int64_t out_head_stride, int32_t* err_flag, msa_stream_t stream);
+msa_status msa_rope_backward(msa_dtype dt, const void* dout, int64_t dout_tok_stride, int64_t dout_head_stride,
+                             int64_t N, int H, int d, const int32_t* pos, const float* rope_cs, int max_len, int rd,
+                             msa_rope_layout layout, void* dx, int64_t dx_tok_stride, int64_t dx_head_stride,
+                             int32_t* err_flag, msa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Paged cache, as msa_paged_append and msa_paged_attn see it.
+ *   K, V     element (page, row, head, x) at page * page_stride + row * row_stride
+ *            + head * head_stride + x (strides in elements, multiples of 16 bytes,
+ *            the same for K and V; no two elements may share an address), 0 <=
+ *            page < num_pages, 0 <= row < page size, page size in {8, 16, 32, 64,
+ *            128, 256}, d in {64, 128}.  So pages may be [page, row, head, d] or
+ *            [page, head, row, d], and K and V may be halves of one tensor.
+ *   block_table int32 [B, max_pages]: cache position t of sequence b is row t %
+ *            page of page block_table[b, t / page]; entries past the sequence's
+ *            last page are not read.  Sequences may share pages they only read.
+ *   seq_len  int32 [B]: cached tokens, the new ones included.
+ *   q_off    int64 [B + 1], non-decreasing, in [0, N]: sequence b's new tokens are
+ *            rows [q_off[b], q_off[b+1]) of the packed tensors, at cache positions
+ *            seq_len[b] - n .. seq_len[b] - 1 (n of them).  A sequence may have
+ *            none.  Rows outside every sequence are neither read nor written.
+ * Device flags of both: MSA_FLAG_OFFSETS for offsets that decrease or leave
+ * [0, N], MSA_FLAG_INDEX_OOB for a page outside [0, num_pages) or a length
+ * outside [0, max_pages * page].
+ *
+ * msa_paged_append writes the new tokens' k (rotated) and v into their cache
+ * rows and, unless q is NULL, the rotated queries into q_out.  A token's rotary
+ * position is pos[n], or its cache position where pos is NULL; rope_cs NULL
+ * leaves k and q unrotated (max_len, rd and layout are then ignored).
+ *   q, q_out [N, Hq, d], k, v [N, Hkv, d], dtype dt: heads d apart, token strides
+ *            in elements (multiples of 16 bytes).  q_out may be q itself.
+ *   The pages written must not be shared by sequences of the call, and k, v and
+ *   q must not lie in them.  Appending the same tokens again writes the same.
+ * A token whose page, position or offsets are out of range is skipped and
+ * flagged (a token before position 0 raises MSA_FLAG_OFFSETS).
+ * ---------------------------------------------------------------------- */
+msa_status msa_paged_append(msa_dtype dt, const void* q, int64_t q_tok_stride, void* q_out, int64_t q_out_tok_stride,
+                            int Hq, const void* k, int64_t k_tok_stride, const void* v, int64_t v_tok_stride,
+                            int64_t N, int64_t B, const int64_t* q_off, int Hkv, int d, const int32_t* pos,
+                            const float* rope_cs, int max_len, int rd, msa_rope_layout layout, void* K, void* V,
+                            int64_t num_pages, int page, int64_t page_stride, int64_t row_stride, int64_t head_stride,
+                            const int32_t* block_table, int max_pages, const int32_t* seq_len, int32_t* err_flag,
+                            msa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The layer's attention with the local part in a paged cache: new token i of
+ * sequence b (of n), at position pos = seq_len[b] - n + i, attends over its
+ * sequence's selected memory rows (all visible) and cached rows [0, pos]:
+ *   O = softmax(scale q K^T) V,  lse = log sum exp(scale q . k)
+ * Decoding steps (n = 1), drafts, parts of prompts and mixtures of them are one
+ * call; the result of a token does not depend on how the batch is put together
+ * beyond the order of fp32 sums.
+ *   Q        [N, Hq, d] dtype dt, heads d apart, token stride in elements;
+ *   max_q    an upper bound of every sequence's n (a sequence above it is
+ *            skipped and raises MSA_FLAG_OFFSETS); it selects the kernel
+ *   k, topk_idx int32 [B, k], doc_chunk_off int64 [D + 1], Kbar, Vbar [C, Hkv, d],
+ *   Mmax     the selected documents, as in msa_sparse_attn_indexed (device memory
+ *            only: MSA_ERR_UNSUPPORTED for page-locked host memory); k = 0: no
+ *            memory rows, and these arguments are ignored
+ *   O        [N, Hq, d] dtype dt, dense;  lse fp32 [Hq, N] or NULL
+ *   scale    <= 0 means 1/sqrt(d)
+ * A token that sees no key (a position before 0, no memory rows) gets O = 0 and
+ * lse = -inf.  Cached rows at positions the sequence has (below seq_len) and bank
+ * rows must hold finite values; every other row of a page may hold anything.
+ * Supported: Hq % Hkv == 0, at most 64 query heads per KV head.  bf16 runs on the
+ * tensor cores, fp32 in fp32.  The result does not depend on timing: partial sums
+ * are merged in a fixed order.
+ * Workspace: msa_paged_attn_workspace_size bytes (for the same arguments and the
+ * device that runs the call current), 16-byte aligned, not initialised, not kept;
+ * calls that may overlap on the GPU need one each.
+ * Device flags: the above, those of the selection (MSA_FLAG_INDEX_OOB for a
+ * document outside [0, D), MSA_FLAG_OVERFLOW past Mmax rows), MSA_FLAG_TIMEOUT.
+ * ---------------------------------------------------------------------- */
+size_t msa_paged_attn_workspace_size(msa_dtype dt, int64_t B, int max_q, int Hq, int Hkv, int d, int k, int Mmax);
+msa_status msa_paged_attn(msa_dtype dt, const void* Q, int64_t q_tok_stride, int64_t N, int64_t B, int max_q,
+                          const int64_t* q_off, int Hq, int Hkv, int d, const void* K, const void* V,
+                          int64_t num_pages, int page, int64_t page_stride, int64_t row_stride, int64_t head_stride,
+                          const int32_t* block_table, int max_pages, const int32_t* seq_len, const int32_t* topk_idx,
+                          int k, const int64_t* doc_chunk_off, int64_t D, int64_t C, const void* Kbar,
+                          const void* Vbar, int Mmax, float scale, void* O, float* lse, void* ws, size_t ws_bytes,
+                          int32_t* err_flag, msa_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -15,6 +15,8 @@ from . import _lib
 
 F32, BF16 = 0, 1
 FLAG_INDEX_OOB, FLAG_OFFSETS, FLAG_TIMEOUT, FLAG_OVERFLOW = 1, 2, 4, 8
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1  # msa_rope_layout
+ROPE_SCALES = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}  # MSA_ROPE_SCALE_*
 DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
 
 
@@ -279,3 +281,152 @@ def gated_delta_rule(q, k, v, g, beta, o, h0=None, hT=None, scale=0.0, stream=No
     f = torch.float32
     _call("msa_gated_delta_rule", _dt(q), _p(q), _p(k, q.dtype), _p(v, q.dtype), _p(g, f), _p(beta, f), B, T, Hk, Hv,
           dk, dv, _p(h0, f), float(scale), _p(o, q.dtype), _p(hT, f), _s(stream))
+
+
+# ---- rotary positions and the paged cache of the local keys and values
+
+
+def _rows(t, name, dims, dtype=None):
+    """Device pointer of a CUDA tensor of `dims` dimensions whose last one is contiguous (the
+    library takes the other strides)."""
+    if not t.is_cuda:
+        raise ValueError("the MSA library takes CUDA tensors")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"expected {dtype}, got {t.dtype}")
+    if t.dim() != dims:
+        raise ValueError(f"{name} has {t.dim()} dimensions, not {dims}")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    return t.data_ptr()
+
+
+def _head_rows(t, name, dtype=None):
+    """_rows of a [N, H, d] tensor whose heads are d apart."""
+    p = _rows(t, name, 3, dtype)
+    if t.shape[1] > 1 and t.stride(1) != t.shape[2]:
+        raise ValueError(f"the heads of {name} must be contiguous")
+    return p
+
+
+def _shape(t, name, *shape):
+    if t is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {shape}")
+
+
+def _one_device(*tensors):
+    """All tensors (None aside) on the current device: the launch goes to its stream."""
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.is_cuda and t.get_device() != cur:
+            raise ValueError(f"a tensor is on device {t.get_device()}, the current device is {cur}")
+
+
+def rope_table_scaled(method: str, theta: float, rd: int, max_len: int, factor: float = 1.0, orig_len: float = 0.0,
+                      lo: float = 0.0, hi: float = 0.0) -> torch.Tensor:
+    """Host fp32 [max_len, rd/2, 2] table with angles scaled for longer contexts
+    (msa_rope_table_scaled_host); method: a key of ROPE_SCALES."""
+    if method not in ROPE_SCALES:
+        raise ValueError(f"unknown method {method!r}: one of {sorted(ROPE_SCALES)}")
+    out = torch.empty((max(max_len, 0), max(rd, 0) // 2, 2), dtype=torch.float32)
+    _call("msa_rope_table_scaled_host", ROPE_SCALES[method], float(theta), rd, max_len, float(factor),
+          float(orig_len), float(lo), float(hi), out.data_ptr())
+    return out
+
+
+def _rope(fn, x, pos, rope_cs, out, layout, err_flag, stream):
+    N, H, d = x.shape
+    _shape(out, "out", N, H, d)
+    _shape(pos, "pos", N)
+    _shape(rope_cs, "rope_cs", rope_cs.shape[0], rope_cs.shape[1], 2)
+    _one_device(x, pos, rope_cs, out, err_flag)
+    _call(fn, _dt(x), _rows(x, "x", 3), x.stride(0), x.stride(1), N, H, d, _p(pos, torch.int32),
+          _p(rope_cs, torch.float32), rope_cs.shape[0], 2 * rope_cs.shape[1], int(layout),
+          _rows(out, "out", 3, x.dtype), out.stride(0), out.stride(1), _p(err_flag, torch.int32), _s(stream))
+
+
+def rope(x, pos, rope_cs, out, layout=ROPE_HALF, err_flag=None, stream=None):
+    """Rotary positions (msa_rope): the first 2 * rope_cs.shape[1] dimensions of every head of x
+    [N, H, d] rotated by position pos int32 [N] into out (which may be x).  x and out may be
+    strided views; the last dimension is contiguous."""
+    _rope("msa_rope", x, pos, rope_cs, out, layout, err_flag, stream)
+
+
+def rope_backward(dout, pos, rope_cs, dx, layout=ROPE_HALF, err_flag=None, stream=None):
+    """Backward of rope (msa_rope_backward): dx from dout by the transposed rotation."""
+    _rope("msa_rope_backward", dout, pos, rope_cs, dx, layout, err_flag, stream)
+
+
+def _cache(Kpages, Vpages, block_table, seq_len, q_off, dtype):
+    """The cache arguments both paged entry points take, checked."""
+    kp, vp = _rows(Kpages, "Kpages", 4, dtype), _rows(Vpages, "Vpages", 4, dtype)
+    if Kpages.shape != Vpages.shape or Kpages.stride() != Vpages.stride():
+        raise ValueError("Kpages and Vpages must have the same shape and strides")
+    B = seq_len.numel()
+    _shape(q_off, "q_off", B + 1)
+    _shape(block_table, "block_table", B, block_table.shape[-1])
+    ps, rs, hs, _ = Kpages.stride()
+    return kp, vp, (Kpages.shape[0], Kpages.shape[1], ps, rs, hs, _p(block_table, torch.int32), block_table.shape[1],
+                    _p(seq_len, torch.int32))
+
+
+def paged_append(q, k, v, q_off, seq_len, block_table, Kpages, Vpages, rope_cs=None, q_out=None, pos=None,
+                 layout=ROPE_HALF, err_flag=None, stream=None):
+    """New tokens into the paged cache (msa_paged_append): k (rotated) and v [N, Hkv, d] into the
+    pages [num_pages, page, Hkv, d] (any strides) of their sequences, q (rotated) into q_out.
+    q may be None; rope_cs None: no rotation; pos None: cache positions."""
+    N, Hkv, d = k.shape
+    _shape(v, "v", N, Hkv, d)
+    _shape(pos, "pos", N)
+    if tuple(Kpages.shape[2:]) != (Hkv, d):
+        raise ValueError("Kpages must be [num_pages, page, Hkv, d] of k's heads")
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    _one_device(q, k, v, q_off, seq_len, block_table, Kpages, Vpages, rope_cs, q_out, pos, err_flag)
+    qp = qop = None
+    Hq = qs = qos = 0
+    if q is not None:
+        Hq = q.shape[1]
+        _shape(q, "q", N, Hq, d)
+        _shape(q_out, "q_out", N, Hq, d)
+        qp, qop, qs, qos = _head_rows(q, "q", k.dtype), _head_rows(q_out, "q_out", k.dtype), q.stride(0), q_out.stride(0)
+    max_len = rd = 0
+    if rope_cs is not None:
+        max_len, rd = rope_cs.shape[0], 2 * rope_cs.shape[1]
+        _shape(rope_cs, "rope_cs", max_len, rd // 2, 2)
+    kp, vp, cache = _cache(Kpages, Vpages, block_table, seq_len, q_off, k.dtype)
+    _call("msa_paged_append", _dt(k), qp, qs, qop, qos, Hq, _head_rows(k, "k"), k.stride(0),
+          _head_rows(v, "v", k.dtype), v.stride(0), N, seq_len.numel(), _p(q_off, torch.int64), Hkv, d,
+          _p(pos, torch.int32), _p(rope_cs, torch.float32), max_len, rd, int(layout), kp, vp, *cache,
+          _p(err_flag, torch.int32), _s(stream))
+
+
+def paged_attn_workspace_size(dtype, B, max_q, Hq, Hkv, d, k=0, Mmax=0) -> int:
+    return _lib.load().msa_paged_attn_workspace_size(DTYPES[dtype], B, max_q, Hq, Hkv, d, k, Mmax)
+
+
+def paged_attn(Q, q_off, max_q, Kpages, Vpages, block_table, seq_len, O, ws, lse=None, scale=0.0, topk_idx=None,
+               doc_chunk_off=None, Kbar=None, Vbar=None, Mmax=0, err_flag=None, stream=None):
+    """Attention of new tokens over [selected memory rows ++ paged cache] (msa_paged_attn): Q
+    [N, Hq, d] packed by q_off int64 [B + 1] (at most max_q tokens a sequence), pages
+    [num_pages, page, Hkv, d] (any strides), O [N, Hq, d], lse fp32 [Hq, N].  topk_idx int32 [B, k]
+    with doc_chunk_off, Kbar and Vbar adds the selected documents' rows (at most Mmax)."""
+    N, Hq, d = Q.shape
+    Hkv = Kpages.shape[2]
+    if Kpages.shape[-1] != d:
+        raise ValueError("Kpages must be [num_pages, page, Hkv, d] of Q's head size")
+    _shape(O, "O", N, Hq, d)
+    _shape(lse, "lse", Hq, N)
+    _one_device(Q, q_off, Kpages, Vpages, block_table, seq_len, O, ws, lse, topk_idx, doc_chunk_off, Kbar, Vbar,
+                err_flag)
+    B = seq_len.numel()
+    kp, vp, cache = _cache(Kpages, Vpages, block_table, seq_len, q_off, Q.dtype)
+    k = D = C = 0
+    if topk_idx is not None:
+        k, D, C = topk_idx.shape[1], doc_chunk_off.numel() - 1, Kbar.shape[0]
+        _shape(topk_idx, "topk_idx", B, k)
+        _shape(Kbar, "Kbar", C, Hkv, d)
+        _shape(Vbar, "Vbar", C, Hkv, d)
+    _call("msa_paged_attn", _dt(Q), _head_rows(Q, "Q"), Q.stride(0), N, B, max_q, _p(q_off, torch.int64), Hq, Hkv, d,
+          kp, vp, *cache, _p(topk_idx, torch.int32), k, _p(doc_chunk_off, torch.int64), D, C,
+          _p(Kbar, Q.dtype, host_ok=True), _p(Vbar, Q.dtype, host_ok=True), Mmax, float(scale), _p(O, Q.dtype),
+          _p(lse, torch.float32), _p(ws), ws.numel() * ws.element_size(), _p(err_flag, torch.int32), _s(stream))

@@ -59,6 +59,19 @@ SIGNATURES = {
     "msa_state_gather_sum": (C.c_int, [C.c_int, P, I64, I64, P, I64, C.c_int, P, P, P]),
     "msa_gated_delta_rule": (C.c_int, [C.c_int, P, P, P, P, P, I64, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int,
                                        P, F32, P, P, P]),
+    "msa_rope_table_scaled_host": (C.c_int, [C.c_int, C.c_double, C.c_int, C.c_int, C.c_double, C.c_double,
+                                             C.c_double, C.c_double, P]),
+    "msa_rope": (C.c_int, [C.c_int, P, I64, I64, I64, C.c_int, C.c_int, P, P, C.c_int, C.c_int, C.c_int,
+                           P, I64, I64, P, P]),
+    "msa_rope_backward": (C.c_int, [C.c_int, P, I64, I64, I64, C.c_int, C.c_int, P, P, C.c_int, C.c_int, C.c_int,
+                                    P, I64, I64, P, P]),
+    "msa_paged_append": (C.c_int, [C.c_int, P, I64, P, I64, C.c_int, P, I64, P, I64, I64, I64, P, C.c_int, C.c_int,
+                                   P, P, C.c_int, C.c_int, C.c_int, P, P, I64, C.c_int, I64, I64, I64,
+                                   P, C.c_int, P, P, P]),
+    "msa_paged_attn_workspace_size": (SZ, [C.c_int, I64, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int]),
+    "msa_paged_attn": (C.c_int, [C.c_int, P, I64, I64, I64, C.c_int, P, C.c_int, C.c_int, C.c_int, P, P,
+                                 I64, C.c_int, I64, I64, I64, P, C.c_int, P, P, C.c_int, P, I64, I64, P,
+                                 P, C.c_int, F32, P, P, P, SZ, P, P]),
 }
 
 _lib = None

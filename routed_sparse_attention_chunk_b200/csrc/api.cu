@@ -184,6 +184,104 @@ msa_status run_indexed(msa_dtype dt, const void* Q, const void* Kloc, const void
   return cuda_status(launch_attn(dt, a, s));
 }
 
+// ---- paged cache
+
+inline bool page_ok(int page) { return page >= 8 && page <= 256 && (page & (page - 1)) == 0; }
+inline bool vec_stride(msa_dtype dt, int64_t s) { return s % (dt == MSA_F32 ? 4 : 8) == 0; }  // 16 bytes
+
+// Strides of a cache whose elements do not overlap: each dimension, from the
+// narrowest stride up, steps past the extent of the ones below it.
+bool strides_apart(int64_t inner, int64_t s0, int64_t n0, int64_t s1, int64_t n1, int64_t s2, int64_t n2) {
+  int64_t st[3] = {s0, s1, s2}, n[3] = {n0, n1, n2};
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 3; ++j)
+      if (st[j] < st[i]) {
+        const int64_t a = st[i], b = n[i];
+        st[i] = st[j];
+        n[i] = n[j];
+        st[j] = a;
+        n[j] = b;
+      }
+  int64_t extent = inner;
+  for (int i = 0; i < 3; ++i) {
+    if (n[i] <= 1) continue;
+    if (st[i] < extent || st[i] > (int64_t(1) << 46) / n[i]) return false;
+    extent = st[i] * (n[i] - 1) + extent;
+  }
+  return true;
+}
+
+// The arguments the append and the attention share.
+msa_status check_paged(msa_dtype dt, int64_t N, int64_t B, const int64_t* q_off, int Hkv, int d, const void* K,
+                       const void* V, int64_t num_pages, int page, int64_t page_stride, int64_t row_stride,
+                       int64_t head_stride, const int32_t* table, int max_pages, const int32_t* seq_len) {
+  if (!dtype_ok(dt) || N < 0 || B < 0 || Hkv < 1 || num_pages < 1 || max_pages < 1 || page < 1)
+    return MSA_ERR_INVALID_ARG;
+  if (N > kMaxIndex || B > kMaxIndex || num_pages >= kMaxIndex || (int64_t)max_pages * page > kMaxIndex)
+    return MSA_ERR_INVALID_ARG;
+  if (!head_dim_ok(d) || !page_ok(page) || Hkv > 65535) return MSA_ERR_UNSUPPORTED;
+  if (N == 0 || B == 0) return MSA_OK;  // nothing to read: pointers of empty tensors may be NULL
+  if (!q_off || !K || !V || !table || !seq_len) return MSA_ERR_INVALID_ARG;
+  if (!aligned16(K) || !aligned16(V)) return MSA_ERR_INVALID_ARG;
+  if (!vec_stride(dt, page_stride) || !vec_stride(dt, row_stride) || !vec_stride(dt, head_stride) ||
+      !strides_apart(d, page_stride, num_pages, row_stride, page, head_stride, Hkv))
+    return MSA_ERR_INVALID_ARG;
+  return MSA_OK;
+}
+msa_status check_rotary(int d, int max_len, int rd, int layout) {
+  if (max_len < 1 || rd < 2 || rd > d || (rd & 1) || (layout != MSA_ROPE_HALF && layout != MSA_ROPE_INTERLEAVED))
+    return MSA_ERR_INVALID_ARG;
+  return rd % 16 != 0 ? MSA_ERR_UNSUPPORTED : MSA_OK;  // whole 16-byte vectors on both sides of a pair
+}
+msa_status run_rope(msa_dtype dt, const void* x, int64_t x_ts, int64_t x_hs, int64_t N, int H, int d,
+                    const int32_t* pos, const float* cs, int max_len, int rd, int layout, bool transpose, void* out,
+                    int64_t out_ts, int64_t out_hs, int32_t* err_flag, msa_stream_t stream) {
+  if (!dtype_ok(dt) || N < 0 || H < 1 || d < 1) return MSA_ERR_INVALID_ARG;
+  if (N > kMaxIndex) return MSA_ERR_INVALID_ARG;
+  if (d % 16 != 0 || d > 1024 || H > 65535) return MSA_ERR_UNSUPPORTED;
+  msa_status st = check_rotary(d, max_len, rd, layout);
+  if (st != MSA_OK) return st;
+  if (N == 0) return MSA_OK;  // nothing to read: pointers of empty tensors may be NULL
+  if (!x || !pos || !out || !cs || !aligned16(cs) || !aligned16(x) || !aligned16(out)) return MSA_ERR_INVALID_ARG;
+  if (x_ts < 0 || x_hs < 0 || !vec_stride(dt, x_ts) || !vec_stride(dt, x_hs) || !vec_stride(dt, out_ts) ||
+      !vec_stride(dt, out_hs) || !strides_apart(d, out_ts, N, out_hs, H, 0, 1))
+    return MSA_ERR_INVALID_ARG;
+  if (x == out && ((N > 1 && x_ts != out_ts) || (H > 1 && x_hs != out_hs))) return MSA_ERR_INVALID_ARG;
+  RopeArgs a{x, x_ts, x_hs, N, H, d, pos, cs, max_len, rd, layout == MSA_ROPE_INTERLEAVED, transpose, out, out_ts,
+             out_hs, err_flag};
+  return cuda_status(launch_rope(dt, a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// Workspace of msa_paged_attn: the segment plan (k > 0), then the partial results.
+struct PagedWs {
+  int Smax;
+  int32_t *seg_row, *nseg, *mem_len;
+  uint8_t* seg_cnt;
+  float* part;
+  size_t bytes;
+};
+PagedWs paged_ws_layout(void* base, msa_dtype dt, int64_t B, int max_q, int Hq, int Hkv, int d, int k, int Mmax) {
+  PagedWs w{};
+  size_t rows = 0, cnts = 0, per_b = 0;
+  if (k > 0) {
+    w.Smax = plan_smax(Mmax, k);
+    rows = round_up(sizeof(int32_t) * (size_t)B * w.Smax, 256);
+    cnts = round_up((size_t)B * w.Smax, 256);
+    per_b = round_up(sizeof(int32_t) * (size_t)B, 256);
+  }
+  const size_t plan = rows + cnts + 2 * per_b;
+  w.bytes = plan + round_up(paged_attn_partial_bytes(dt, Hq, Hkv, d, max_q), 256);
+  if (base) {
+    char* p = static_cast<char*>(base);
+    w.seg_row = reinterpret_cast<int32_t*>(p);
+    w.seg_cnt = reinterpret_cast<uint8_t*>(p + rows);
+    w.nseg = reinterpret_cast<int32_t*>(p + rows + cnts);
+    w.mem_len = reinterpret_cast<int32_t*>(p + rows + cnts + per_b);
+    w.part = reinterpret_cast<float*>(p + plan);
+  }
+  return w;
+}
+
 }  // namespace
 
 namespace msa {
@@ -222,6 +320,48 @@ msa_status msa_rope_table_host(double theta, int d, int max_len, float* host_out
       const double ang = (double)p * pow(theta, -2.0 * (double)i / (double)d);
       host_out[((size_t)p * half + i) * 2] = (float)cos(ang);
       host_out[((size_t)p * half + i) * 2 + 1] = (float)sin(ang);
+    }
+  }
+  return MSA_OK;
+}
+
+msa_status msa_rope_table_scaled_host(int method, double theta, int rd, int max_len, double factor, double orig_len,
+                                      double lo, double hi, float* host_out) {
+  if (!host_out || rd < 2 || (rd & 1) || max_len < 1 || !(theta > 0.0)) return MSA_ERR_INVALID_ARG;
+  if (method < MSA_ROPE_SCALE_NONE || method > MSA_ROPE_SCALE_BANDS) return MSA_ERR_INVALID_ARG;
+  if (method != MSA_ROPE_SCALE_NONE && !(factor >= 1.0 && isfinite(factor))) return MSA_ERR_INVALID_ARG;
+  const bool ramp = method == MSA_ROPE_SCALE_YARN || method == MSA_ROPE_SCALE_BANDS;
+  // both ramps need the lengths they start from and two distinct, ordered bounds
+  if (ramp && !(orig_len > 0.0 && isfinite(orig_len) && lo > 0.0 && hi > lo && isfinite(hi))) return MSA_ERR_INVALID_ARG;
+  if (method == MSA_ROPE_SCALE_YARN && !(theta > 1.0)) return MSA_ERR_INVALID_ARG;
+  if (method == MSA_ROPE_SCALE_NTK && rd < 4) return MSA_ERR_INVALID_ARG;  // its exponent is rd / (rd - 2)
+  const int half = rd / 2;
+  const double pi = 3.14159265358979323846;
+  const double base = method == MSA_ROPE_SCALE_NTK ? theta * pow(factor, (double)rd / (rd - 2.0)) : theta;
+  const double mag = method == MSA_ROPE_SCALE_YARN ? 0.1 * log(factor) + 1.0 : 1.0;
+  double first = 0.0, last = 0.0;
+  if (method == MSA_ROPE_SCALE_YARN) {
+    // the dimension that turns r times over orig_len positions: i = rd ln(orig_len / (2 pi r)) / (2 ln theta)
+    first = fmax(floor(rd * log(orig_len / (2.0 * pi * hi)) / (2.0 * log(theta))), 0.0);
+    last = fmin(ceil(rd * log(orig_len / (2.0 * pi * lo)) / (2.0 * log(theta))), rd - 1.0);
+    if (last <= first) last = first + 0.001;
+  }
+  for (int i = 0; i < half; ++i) {
+    double freq = pow(base, -2.0 * (double)i / (double)rd);
+    if (method == MSA_ROPE_SCALE_LINEAR) {
+      freq /= factor;
+    } else if (method == MSA_ROPE_SCALE_YARN) {
+      const double t = fmin(fmax((i - first) / (last - first), 0.0), 1.0);  // 0: kept, 1: interpolated
+      freq = freq * (1.0 - t) + freq / factor * t;
+    } else if (method == MSA_ROPE_SCALE_BANDS) {
+      const double turns = orig_len * freq / (2.0 * pi);
+      const double t = fmin(fmax((turns - lo) / (hi - lo), 0.0), 1.0);  // 1: kept, 0: interpolated
+      freq = freq * t + freq / factor * (1.0 - t);
+    }
+    for (int p = 0; p < max_len; ++p) {
+      const double ang = (double)p * freq;
+      host_out[((size_t)p * half + i) * 2] = (float)(mag * cos(ang));
+      host_out[((size_t)p * half + i) * 2 + 1] = (float)(mag * sin(ang));
     }
   }
   return MSA_OK;
@@ -531,6 +671,131 @@ msa_status msa_state_gather_sum(msa_dtype dt, const void* states, int64_t D, int
   if (!aligned16(states) || !aligned16(S_ext) || !device_readable(states)) return MSA_ERR_INVALID_ARG;
   return cuda_status(launch_state_sum(dt, states, D, S, topk_idx, B, k, S_ext, err_flag,
                                       reinterpret_cast<cudaStream_t>(stream)));
+}
+
+msa_status msa_rope(msa_dtype dt, const void* x, int64_t x_tok_stride, int64_t x_head_stride, int64_t N, int H, int d,
+                    const int32_t* pos, const float* rope_cs, int max_len, int rd, msa_rope_layout layout, void* out,
+                    int64_t out_tok_stride, int64_t out_head_stride, int32_t* err_flag, msa_stream_t stream) {
+  return run_rope(dt, x, x_tok_stride, x_head_stride, N, H, d, pos, rope_cs, max_len, rd, layout, false, out,
+                  out_tok_stride, out_head_stride, err_flag, stream);
+}
+
+msa_status msa_rope_backward(msa_dtype dt, const void* dout, int64_t dout_tok_stride, int64_t dout_head_stride,
+                             int64_t N, int H, int d, const int32_t* pos, const float* rope_cs, int max_len, int rd,
+                             msa_rope_layout layout, void* dx, int64_t dx_tok_stride, int64_t dx_head_stride,
+                             int32_t* err_flag, msa_stream_t stream) {
+  return run_rope(dt, dout, dout_tok_stride, dout_head_stride, N, H, d, pos, rope_cs, max_len, rd, layout, true, dx,
+                  dx_tok_stride, dx_head_stride, err_flag, stream);
+}
+
+msa_status msa_paged_append(msa_dtype dt, const void* q, int64_t q_tok_stride, void* q_out, int64_t q_out_tok_stride,
+                            int Hq, const void* k, int64_t k_tok_stride, const void* v, int64_t v_tok_stride,
+                            int64_t N, int64_t B, const int64_t* q_off, int Hkv, int d, const int32_t* pos,
+                            const float* rope_cs, int max_len, int rd, msa_rope_layout layout, void* K, void* V,
+                            int64_t num_pages, int page, int64_t page_stride, int64_t row_stride, int64_t head_stride,
+                            const int32_t* block_table, int max_pages, const int32_t* seq_len, int32_t* err_flag,
+                            msa_stream_t stream) {
+  msa_status st = check_paged(dt, N, B, q_off, Hkv, d, K, V, num_pages, page, page_stride, row_stride, head_stride,
+                              block_table, max_pages, seq_len);
+  if (st != MSA_OK) return st;
+  if (rope_cs) {
+    st = check_rotary(d, max_len, rd, layout);
+    if (st != MSA_OK) return st;
+  }
+  if (N == 0 || B == 0) return MSA_OK;
+  if (!aligned16(rope_cs) || !k || !v || !aligned16(k) || !aligned16(v) || k_tok_stride < 0 || v_tok_stride < 0 ||
+      !vec_stride(dt, k_tok_stride) || !vec_stride(dt, v_tok_stride))
+    return MSA_ERR_INVALID_ARG;
+  if (q) {
+    if (Hq < 1 || !q_out || !aligned16(q) || !aligned16(q_out) || q_tok_stride < 0 || !vec_stride(dt, q_tok_stride) ||
+        !vec_stride(dt, q_out_tok_stride) || (N > 1 && q_out_tok_stride < (int64_t)Hq * d))
+      return MSA_ERR_INVALID_ARG;
+    if (q == q_out && N > 1 && q_tok_stride != q_out_tok_stride) return MSA_ERR_INVALID_ARG;
+    if (Hq > 65535) return MSA_ERR_UNSUPPORTED;
+  }
+  PagedAppendArgs a{};
+  a.p = PagedBatch{q_off, seq_len, block_table, nullptr, N, B, 0, max_pages, page, 0, Hkv, num_pages, err_flag};
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_ts = q_tok_stride;
+  a.k_ts = k_tok_stride;
+  a.v_ts = v_tok_stride;
+  a.qo_ts = q_out_tok_stride;
+  a.Hq = Hq;
+  a.d = d;
+  a.pos = pos;
+  a.cs = rope_cs;
+  a.max_len = max_len;
+  a.rd = rd;
+  a.interleaved = layout == MSA_ROPE_INTERLEAVED;
+  a.q_out = q_out;
+  a.K = K;
+  a.V = V;
+  a.page_stride = page_stride;
+  a.row_stride = row_stride;
+  a.head_stride = head_stride;
+  return cuda_status(launch_paged_append(dt, a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t msa_paged_attn_workspace_size(msa_dtype dt, int64_t B, int max_q, int Hq, int Hkv, int d, int k, int Mmax) {
+  if (!dtype_ok(dt) || B < 0 || max_q < 1 || Hkv < 1 || Hq < Hkv || d < 1 || k < 0 || k > 65535 || Mmax < 0) return 0;
+  return paged_ws_layout(nullptr, dt, B, max_q, Hq, Hkv, d, k, Mmax).bytes;
+}
+
+msa_status msa_paged_attn(msa_dtype dt, const void* Q, int64_t q_tok_stride, int64_t N, int64_t B, int max_q,
+                          const int64_t* q_off, int Hq, int Hkv, int d, const void* K, const void* V,
+                          int64_t num_pages, int page, int64_t page_stride, int64_t row_stride, int64_t head_stride,
+                          const int32_t* block_table, int max_pages, const int32_t* seq_len, const int32_t* topk_idx,
+                          int k, const int64_t* doc_chunk_off, int64_t D, int64_t C, const void* Kbar,
+                          const void* Vbar, int Mmax, float scale, void* O, float* lse, void* ws, size_t ws_bytes,
+                          int32_t* err_flag, msa_stream_t stream) {
+  msa_status st = check_paged(dt, N, B, q_off, Hkv, d, K, V, num_pages, page, page_stride, row_stride, head_stride,
+                              block_table, max_pages, seq_len);
+  if (st != MSA_OK) return st;
+  if (max_q < 1 || Hq < 1 || Hq % Hkv != 0 || k < 0 || Mmax < 0) return MSA_ERR_INVALID_ARG;
+  if (Hq / Hkv > 64 || Hq > 65535) return MSA_ERR_UNSUPPORTED;
+  if (N == 0 || B == 0) return MSA_OK;
+  if (!Q || !aligned16(Q) || q_tok_stride < 0 || !vec_stride(dt, q_tok_stride)) return MSA_ERR_INVALID_ARG;
+  if (!O || !aligned16(O)) return MSA_ERR_INVALID_ARG;
+  if (k > 0) {
+    st = check_indexed(topk_idx, k, doc_chunk_off, D, C, Kbar, Vbar);
+    if (st != MSA_OK) return st;
+    if (Mmax > kMaxIndex - 8 * 65536) return MSA_ERR_INVALID_ARG;
+  }
+  const PagedWs w = paged_ws_layout(ws, dt, B, max_q, Hq, Hkv, d, k, Mmax);
+  if (!ws || ws_bytes < w.bytes || !aligned16(ws)) return MSA_ERR_WORKSPACE;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (k > 0) {
+    if (!device_readable(Kbar) || !device_readable(Vbar)) return MSA_ERR_INVALID_ARG;
+    if (host_resident(Kbar) || host_resident(Vbar)) return MSA_ERR_UNSUPPORTED;
+    PlanArgs pa{topk_idx, B, k, doc_chunk_off, D, C, Mmax, w.Smax, w.seg_row, w.seg_cnt, w.nseg, w.mem_len, err_flag, k};
+    if (launch_plan(pa, s) != cudaSuccess) return MSA_ERR_CUDA;
+  }
+  PagedAttnArgs a{};
+  a.p = PagedBatch{q_off, seq_len, block_table, k > 0 ? w.nseg : nullptr, N, B, max_q, max_pages, page,
+                   w.Smax, Hkv, num_pages, err_flag};
+  a.Q = Q;
+  a.q_ts = q_tok_stride;
+  a.Hq = Hq;
+  a.d = d;
+  a.K = K;
+  a.V = V;
+  // a dimension of one element may come with any stride: give the tensor maps a plain one
+  a.head_stride = Hkv == 1 ? d : head_stride;
+  a.row_stride = row_stride;
+  a.page_stride = num_pages == 1 ? (int64_t)Hkv * page * d : page_stride;
+  const bool bank = k > 0 && C > 0;  // an empty bank has no rows to read
+  a.Kbar = bank ? Kbar : nullptr;
+  a.Vbar = bank ? Vbar : nullptr;
+  a.C = C;
+  a.seg_row = w.seg_row;
+  a.seg_cnt = w.seg_cnt;
+  a.scale = scale > 0.f ? scale : 1.0f / sqrtf((float)d);
+  a.O = O;
+  a.lse = lse;
+  a.part = w.part;
+  return cuda_status(launch_paged_attn(dt, a, s));
 }
 
 }  // extern "C"

@@ -245,4 +245,75 @@ bool attn_indexed_applies(msa_dtype dt, const AttnArgs& a);
 // Workspace of the decode kernel when the memory rows come through a plan of Smax segments.
 size_t attn_indexed_workspace_size(int64_t B, int Tq, int Lloc, int Hq, int Hkv, int Smax);
 
+// ---- paged cache of the local keys and values
+
+// Rotary positions (rope.cu): the first rd dimensions of every head of x
+// [N, H, d] (row and head strides in elements) rotated by the table row of the
+// token's position into out; transpose: the transposed rotation (the gradient).
+struct RopeArgs {
+  const void* x;
+  int64_t x_ts, x_hs;
+  int64_t N;
+  int H, d;
+  const int32_t* pos;
+  const float* cs;  // [max_len, rd / 2, 2]
+  int max_len, rd;
+  bool interleaved, transpose;
+  void* out;
+  int64_t out_ts, out_hs;
+  int32_t* err_flag;
+};
+cudaError_t launch_rope(msa_dtype dt, const RopeArgs& a, cudaStream_t s);
+
+// A batch of ragged sequences over a paged cache: sequence b owns rows
+// [q_off[b], q_off[b + 1]) of the packed tokens and cache positions
+// [0, seq_len[b]) through its row of the block table.
+struct PagedBatch {
+  const int64_t* q_off;    // [B + 1]
+  const int32_t* seq_len;  // [B]
+  const int32_t* table;    // [B, max_pages]
+  const int32_t* nseg;     // [B]: segments of the memory plan, or null
+  int64_t N, B;
+  int max_q, max_pages, page, Smax, Hkv;
+  int64_t num_pages;
+  int32_t* err_flag;
+};
+
+// Append of new keys and values (paged_append.cu), with the rotation of q and k.
+struct PagedAppendArgs {
+  PagedBatch p;
+  const void *q, *k, *v;  // q may be null
+  int64_t q_ts, k_ts, v_ts, qo_ts;  // token strides; heads are d apart
+  int Hq, d;
+  const int32_t* pos;  // [N] rotary positions, or null: the cache positions
+  const float* cs;     // null: no rotation
+  int max_len, rd;
+  bool interleaved;
+  void* q_out;
+  void *K, *V;
+  int64_t page_stride, row_stride, head_stride;
+};
+cudaError_t launch_paged_append(msa_dtype dt, const PagedAppendArgs& a, cudaStream_t s);
+
+// Attention of the new tokens over [selected memory rows ++ cached tokens].
+struct PagedAttnArgs {
+  PagedBatch p;
+  const void* Q;  // [N, Hq, d], token stride q_ts
+  int64_t q_ts;
+  int Hq, d;
+  const void *K, *V;
+  int64_t page_stride, row_stride, head_stride;
+  const void *Kbar, *Vbar;  // bank [C, Hkv, d] (null: no memory rows)
+  int64_t C;
+  const int32_t* seg_row;
+  const uint8_t* seg_cnt;
+  float scale;
+  void* O;     // [N, Hq, d]
+  float* lse;  // [Hq, N] or null
+  float* part;  // workspace: two partial results per CTA
+};
+// Bytes of the partial results' workspace for this shape on the current device.
+size_t paged_attn_partial_bytes(msa_dtype dt, int Hq, int Hkv, int d, int max_q);
+cudaError_t launch_paged_attn(msa_dtype dt, const PagedAttnArgs& a, cudaStream_t s);
+
 }  // namespace msa

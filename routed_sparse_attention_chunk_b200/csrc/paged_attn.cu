@@ -1,0 +1,316 @@
+// Attention of new tokens over [selected memory rows ++ cached tokens], the cached
+// keys and values in pages: O = softmax(scale q K^T) V over the rows of the
+// documents selected for the token's sequence and the cached positions up to the
+// token's own.  This file holds the dispatcher, the kernel that merges items cut
+// by the work split (paged_sched.cuh) and the fp32 kernel; bf16 runs on the
+// tensor cores (paged_decode.cu, paged_prefill.cu).
+//
+// The fp32 kernel is a single pass over the keys with running row maxima and sums:
+// 256 threads own 16 x RPT query rows (RPT = 1 for a few rows per KV head, 4
+// otherwise), keys come through shared memory 32 at a time, and a thread keeps an
+// RPT x 2 block of scores and an RPT x DH / 16 block of the output in registers.
+// All arithmetic is fp32 FMA; scores are compared and subtracted unscaled, so the
+// exponent's argument (s - max) * scale carries only its own rounding.
+#include <math.h>
+
+#include "common.cuh"
+#include "internal.h"
+#include "paged_sched.cuh"
+#include "tma_host.h"
+
+namespace msa {
+
+cudaError_t launch_paged_decode(const PagedAttnArgs& a, cudaStream_t s);
+cudaError_t launch_paged_prefill(const PagedAttnArgs& a, cudaStream_t s);
+
+namespace paged {
+namespace {
+
+constexpr int kSub = 32;  // keys per step of the fp32 kernel
+constexpr int kF32Threads = 256;
+
+template <int DH, int RPT>
+struct F32Smem {
+  static constexpr int RB = 16 * RPT;
+  float Q[RB][DH + 4];
+  float K[kSub][DH + 4];
+  float V[kSub][DH + 4];
+  float P[RB][kSub + 4];
+  int64_t row[kKeys];  // element offset of each key of the tile in its tensor, -1: no key
+  Start st;
+};
+
+template <int DH, int RPT>
+__global__ void __launch_bounds__(kF32Threads) paged_f32_kernel(PagedAttnArgs a, int TB, Mark* marks, float* slots) {
+  using S = F32Smem<DH, RPT>;
+  constexpr int RB = S::RB, DPT = DH / 16;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  S& sm = *reinterpret_cast<S*>(smem_raw);
+  const PagedBatch& p = a.p;
+  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+  const int G = a.Hq / p.Hkv;
+  pdl_wait();
+  find_start(p, TB, blockIdx.x, gridDim.x, blockIdx.x == 0, &sm.st);
+  if (tid == 0) leave_mark(&sm.st, marks + blockIdx.x);
+  pdl_trigger();
+  if (!sm.st.any) return;
+  const float sl2 = a.scale * 1.4426950408889634f;
+  const float* Q = reinterpret_cast<const float*>(a.Q);
+
+  for (Walk w(p, TB, &sm.st); w.more(); w.next(p, TB)) {
+    const Seq& s = w.s;
+    const int tb0 = w.i * TB;
+    __syncthreads();  // the previous segment's readers are done
+    for (int e = tid; e < RB * (DH / 4); e += kF32Threads) {
+      const int r = e / (DH / 4), c = (e - r * (DH / 4)) * 4;
+      const int t = tb0 + r / G;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < TB * G && t < s.nq)
+        v = __ldg(reinterpret_cast<const float4*>(Q + (s.q0 + t) * a.q_ts + (w.g * G + r % G) * DH + c));
+      *reinterpret_cast<float4*>(&sm.Q[r][c]) = v;
+    }
+    int pos[RPT];  // last visible cache position of this thread's rows
+    float m_run[RPT], l_run[RPT], o[RPT][DPT];
+#pragma unroll
+    for (int j = 0; j < RPT; ++j) {
+      const int r = ty * RPT + j, t = tb0 + r / G;
+      pos[j] = r < TB * G && t < s.nq ? s.len - s.nq + t : -1;
+      m_run[j] = -INFINITY;
+      l_run[j] = 0.f;
+#pragma unroll
+      for (int c = 0; c < DPT; ++c) o[j][c] = 0.f;
+    }
+    const int last = s.len - s.nq + min(tb0 + TB, s.nq) - 1;  // the block's last visible position
+
+    for (int t = w.t0; t < w.t0 + w.n; ++t) {
+      const bool mem = t < s.nm;
+      const int key0 = mem ? 0 : (t - s.nm) * kKeys;
+      if (tid < kKeys) {
+        int64_t off = -1;
+        if (mem) {
+          const int sg = t * kTileSegs + tid / kSegRows, x = tid % kSegRows;
+          if (sg < p.Smax && x < __ldg(a.seg_cnt + w.b * p.Smax + sg))
+            off = ((int64_t)(__ldg(a.seg_row + w.b * p.Smax + sg) + x) * p.Hkv + w.g) * DH;
+        } else if (key0 + tid <= last) {
+          const int at = key0 + tid, pi = at / p.page;
+          const int64_t pg = __ldg(p.table + w.b * p.max_pages + pi);
+          if (pg >= 0 && pg < p.num_pages)
+            off = pg * a.page_stride + (at - pi * p.page) * a.row_stride + w.g * a.head_stride;
+          else
+            raise_flag(p.err_flag, MSA_FLAG_INDEX_OOB);
+        }
+        sm.row[tid] = off;
+      }
+      const float* Ksrc = reinterpret_cast<const float*>(mem ? a.Kbar : a.K);
+      const float* Vsrc = reinterpret_cast<const float*>(mem ? a.Vbar : a.V);
+      for (int k0 = 0; k0 < kKeys; k0 += kSub) {
+        if (!mem && key0 + k0 > last) break;
+        __syncthreads();  // rows written; the previous step's K, V and P are read
+        for (int e = tid; e < kSub * (DH / 4); e += kF32Threads) {
+          const int r = e / (DH / 4), c = (e - r * (DH / 4)) * 4;
+          const int64_t off = sm.row[k0 + r];
+          float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
+          if (off >= 0) {
+            kv = __ldg(reinterpret_cast<const float4*>(Ksrc + off + c));
+            vv = __ldg(reinterpret_cast<const float4*>(Vsrc + off + c));
+          }
+          *reinterpret_cast<float4*>(&sm.K[r][c]) = kv;
+          *reinterpret_cast<float4*>(&sm.V[r][c]) = vv;
+        }
+        __syncthreads();
+        float sc[RPT][2];
+#pragma unroll
+        for (int j = 0; j < RPT; ++j) sc[j][0] = sc[j][1] = 0.f;
+#pragma unroll 4
+        for (int c = 0; c < DH; c += 4) {
+          const float4 ka = *reinterpret_cast<const float4*>(&sm.K[tx][c]);
+          const float4 kb = *reinterpret_cast<const float4*>(&sm.K[tx + 16][c]);
+#pragma unroll
+          for (int j = 0; j < RPT; ++j) {
+            const float4 q = *reinterpret_cast<const float4*>(&sm.Q[ty * RPT + j][c]);
+            sc[j][0] = fmaf(q.x, ka.x, fmaf(q.y, ka.y, fmaf(q.z, ka.z, fmaf(q.w, ka.w, sc[j][0]))));
+            sc[j][1] = fmaf(q.x, kb.x, fmaf(q.y, kb.y, fmaf(q.z, kb.z, fmaf(q.w, kb.w, sc[j][1]))));
+          }
+        }
+        const bool ha = sm.row[k0 + tx] >= 0, hb = sm.row[k0 + tx + 16] >= 0;
+        const int pa = key0 + k0 + tx, pb = pa + 16;
+#pragma unroll
+        for (int j = 0; j < RPT; ++j) {
+          if (!(ha && (mem || pa <= pos[j]))) sc[j][0] = -INFINITY;
+          if (!(hb && (mem || pb <= pos[j]))) sc[j][1] = -INFINITY;
+          float mx = fmaxf(sc[j][0], sc[j][1]);
+#pragma unroll
+          for (int x = 8; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+          const float m_new = fmaxf(m_run[j], mx);
+          // a row that has seen no key yet keeps weight 0 for everything
+          const float corr = m_run[j] == -INFINITY ? 0.f : exp2f((m_run[j] - m_new) * sl2);
+          const float e0 = sc[j][0] == -INFINITY ? 0.f : exp2f((sc[j][0] - m_new) * sl2);
+          const float e1 = sc[j][1] == -INFINITY ? 0.f : exp2f((sc[j][1] - m_new) * sl2);
+          float sum = e0 + e1;
+#pragma unroll
+          for (int x = 8; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+          l_run[j] = l_run[j] * corr + sum;
+          m_run[j] = m_new;
+#pragma unroll
+          for (int c = 0; c < DPT; ++c) o[j][c] *= corr;
+          sm.P[ty * RPT + j][tx] = e0;
+          sm.P[ty * RPT + j][tx + 16] = e1;
+        }
+        __syncwarp();  // a row's weights are written and read by the same 16 lanes
+        for (int kc = 0; kc < kSub; kc += 4) {
+          float4 pr[RPT];
+#pragma unroll
+          for (int j = 0; j < RPT; ++j) pr[j] = *reinterpret_cast<const float4*>(&sm.P[ty * RPT + j][kc]);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            // weight 0 keeps a masked key out even where its value is not finite
+            float v[DPT];
+#pragma unroll
+            for (int c = 0; c < DPT; c += 4) {
+              const float4 x = *reinterpret_cast<const float4*>(&sm.V[kc + q][(c / 4) * 64 + tx * 4]);
+              v[c] = x.x; v[c + 1] = x.y; v[c + 2] = x.z; v[c + 3] = x.w;
+            }
+#pragma unroll
+            for (int j = 0; j < RPT; ++j) {
+              const float pw = q == 0 ? pr[j].x : q == 1 ? pr[j].y : q == 2 ? pr[j].z : pr[j].w;
+#pragma unroll
+              for (int c = 0; c < DPT; ++c) o[j][c] = pw == 0.f ? o[j][c] : fmaf(pw, v[c], o[j][c]);
+            }
+          }
+        }
+      }
+      __syncthreads();  // this tile's rows are read before the next tile's are written
+    }
+
+    const bool whole = w.whole();
+    float* slot = slots + slot_of(blockIdx.x, w.f, sm.st.f0) * slot_floats(RB, DH);
+#pragma unroll
+    for (int j = 0; j < RPT; ++j) {
+      const int r = ty * RPT + j, t = tb0 + r / G;
+      if (r >= TB * G || t >= s.nq) continue;
+      const int h = w.g * G + r % G;
+      // the sum is 0 only where no key was visible: such a row is 0, its log-sum-exp -inf
+      const float inv = whole ? (l_run[j] == 0.f ? 0.f : 1.f / l_run[j]) : 1.f;
+      float* dst = whole ? reinterpret_cast<float*>(a.O) + ((s.q0 + t) * a.Hq + h) * DH : slot + r * DH;
+#pragma unroll
+      for (int c = 0; c < DPT; c += 4)
+        *reinterpret_cast<float4*>(dst + (c / 4) * 64 + tx * 4) =
+            make_float4(o[j][c] * inv, o[j][c + 1] * inv, o[j][c + 2] * inv, o[j][c + 3] * inv);
+      if (tx == 0) {
+        if (!whole) {
+          slot[RB * DH + 2 * r] = m_run[j];
+          slot[RB * DH + 2 * r + 1] = l_run[j];
+        } else if (a.lse) {
+          a.lse[(int64_t)h * p.N + s.q0 + t] = l_run[j] == 0.f ? -INFINITY : m_run[j] * a.scale + logf(l_run[j]);
+        }
+      }
+    }
+  }
+}
+
+// O = sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s over an item's segments, in the
+// order of the CTAs.  Block x merges the item that border x + 1 is the first to cut
+// (if there is one); block y takes 32 of its rows, a thread four values of a row.
+template <typename T, int DH, bool kQuads>
+__global__ void __launch_bounds__(256) merge_kernel(MergeArgs a) {
+  pdl_wait();
+  const int64_t c = (int64_t)blockIdx.x + 1;
+  const Mark mk = a.marks[c];
+  if (!mk.any || mk.t == 0) return;
+  const Seq s = load_seq(a.p, mk.b);
+  const int64_t start = mk.f0 - mk.t, per = mk.per;
+  const int64_t c0 = start / per, c1 = (start + block_tiles(s, a.TB, mk.i) - 1) / per;
+  if (c0 != c - 1) return;  // an earlier border's block merges this item
+  const int quad = threadIdx.x >> 3;
+  if (quad >= DH / 4) return;
+  const size_t sf = slot_floats(a.rows, DH);
+  const bool late = start != c0 * per;  // the first segment is its CTA's last one, not its first
+#pragma unroll 1
+  for (int j = 0; j < 4; ++j) {
+    const int r = blockIdx.y * 32 + j * 8 + (threadIdx.x & 7);
+    const int t = mk.i * a.TB + r / a.G;
+    if (r >= a.TB * a.G || t >= s.nq) continue;
+    auto slot = [&](int64_t x) { return a.slots + (2 * x + (x == c0 && late ? 1 : 0)) * sf; };
+    float m = -INFINITY;
+#pragma unroll 4
+    for (int64_t x = c0; x <= c1; ++x) m = fmaxf(m, __ldg(slot(x) + a.rows * DH + 2 * r));
+    float l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int64_t x = c0; x <= c1; ++x) {
+      const float* src = slot(x);
+      const float2 ml = __ldg(reinterpret_cast<const float2*>(src + a.rows * DH + 2 * r));
+      const float4 v = __ldg(reinterpret_cast<const float4*>(src + (kQuads ? (quad * a.rows + r) * 4 : r * DH + quad * 4)));
+      const float w = ml.y == 0.f ? 0.f : exp2f((ml.x - m) * a.unit_log2);  // sum 0: no key was visible
+      l += w * ml.y;
+      acc[0] += w * v.x;
+      acc[1] += w * v.y;
+      acc[2] += w * v.z;
+      acc[3] += w * v.w;
+    }
+    const bool seen = l != 0.f;
+    const float inv = seen ? 1.f / l : 0.f;
+    const int h = mk.g * a.G + r % a.G;
+    T* dst = reinterpret_cast<T*>(a.O) + ((s.q0 + t) * a.Hq + h) * DH + quad * 4;
+    if constexpr (sizeof(T) == 4)
+      *reinterpret_cast<float4*>(dst) = make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
+    else
+      *reinterpret_cast<uint2*>(dst) =
+          make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+    if (a.lse && quad == 0)
+      a.lse[(int64_t)h * a.p.N + s.q0 + t] =
+          seen ? (m * a.unit_log2 + log2f(l)) * 0.69314718055994531f : -INFINITY;
+  }
+}
+
+template <int DH, int RPT>
+cudaError_t f32_t(const PagedAttnArgs& a, int TB, cudaStream_t s) {
+  using S = F32Smem<DH, RPT>;
+  cudaError_t e = cudaFuncSetAttribute(paged_f32_kernel<DH, RPT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)sizeof(S));
+  if (e != cudaSuccess) return e;
+  const int grid = 2 * sm_count();
+  Mark* marks = reinterpret_cast<Mark*>(a.part);
+  float* slots = reinterpret_cast<float*>(reinterpret_cast<char*>(a.part) + marks_bytes(grid));
+  count_launch();
+  e = launch_pdl(paged_f32_kernel<DH, RPT>, dim3((unsigned)grid), dim3(kF32Threads), sizeof(S), s, a, TB, marks, slots);
+  if (e != cudaSuccess) return e;
+  MergeArgs m{a.p, marks, slots, S::RB, TB, a.Hq / a.p.Hkv, a.Hq, a.scale * 1.4426950408889634f, a.O, a.lse};
+  return launch_merge(MSA_F32, DH, false, m, grid, s);
+}
+
+// Few rows per KV head: the kernels that hold at most 16 of them.
+bool few_rows(int Hq, int Hkv, int max_q) { return (int64_t)(Hq / Hkv) * max_q <= 16; }
+
+}  // namespace
+
+cudaError_t launch_merge(msa_dtype dt, int d, bool quads, const MergeArgs& a, int grid, cudaStream_t s) {
+  if (grid < 2) return cudaSuccess;
+  const dim3 g((unsigned)(grid - 1), (unsigned)((a.rows + 31) / 32));
+  count_launch();
+  if (dt == MSA_F32) return launch_pdl(d == 64 ? merge_kernel<float, 64, false> : merge_kernel<float, 128, false>, g, dim3(256), 0, s, a);
+  if (quads)
+    return launch_pdl(d == 64 ? merge_kernel<__nv_bfloat16, 64, true> : merge_kernel<__nv_bfloat16, 128, true>, g,
+                      dim3(256), 0, s, a);
+  return launch_pdl(merge_kernel<__nv_bfloat16, 128, false>, g, dim3(256), 0, s, a);
+}
+
+}  // namespace paged
+
+size_t paged_attn_partial_bytes(msa_dtype dt, int Hq, int Hkv, int d, int max_q) {
+  const bool few = paged::few_rows(Hq, Hkv, max_q);
+  const int grid = dt == MSA_F32 ? 2 * sm_count() : sm_count();
+  const int rows = dt == MSA_F32 ? (few ? 16 : 64) : (few && d == 128 ? Hq / Hkv * max_q : 128);
+  return paged::marks_bytes(grid) + 2 * (size_t)grid * paged::slot_floats(rows, d) * sizeof(float);
+}
+
+cudaError_t launch_paged_attn(msa_dtype dt, const PagedAttnArgs& a, cudaStream_t s) {
+  const bool few = paged::few_rows(a.Hq, a.p.Hkv, a.p.max_q);
+  if (dt == MSA_F32) {
+    const int TB = few ? a.p.max_q : 64 / (a.Hq / a.p.Hkv);
+    if (a.d == 64) return few ? paged::f32_t<64, 1>(a, TB, s) : paged::f32_t<64, 4>(a, TB, s);
+    return few ? paged::f32_t<128, 1>(a, TB, s) : paged::f32_t<128, 4>(a, TB, s);
+  }
+  return few && a.d == 128 ? launch_paged_decode(a, s) : launch_paged_prefill(a, s);
+}
+
+}  // namespace msa
