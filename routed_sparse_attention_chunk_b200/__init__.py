@@ -284,41 +284,48 @@ def gated_delta_rule(q, k, v, g, beta, o, h0=None, hT=None, scale=0.0, stream=No
 
 
 # ---- rotary positions and the paged cache of the local keys and values
+# A decoding step calls these for every layer, so each tensor is looked at once.
 
 
-def _rows(t, name, dims, dtype=None):
-    """Device pointer of a CUDA tensor of `dims` dimensions whose last one is contiguous (the
-    library takes the other strides)."""
-    if not t.is_cuda:
-        raise ValueError("the MSA library takes CUDA tensors")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"expected {dtype}, got {t.dtype}")
-    if t.dim() != dims:
-        raise ValueError(f"{name} has {t.dim()} dimensions, not {dims}")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise ValueError(f"the last dimension of {name} must be contiguous")
+def _dev() -> int:
+    """The current device, as the launch and its stream take it."""
+    return torch._C._cuda_getDevice()
+
+
+def _raw_stream(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _at(t, name, dtype, dev, shape=None):
+    """Device pointer of a contiguous tensor of this dtype (and shape) on the current device."""
+    if t is None:
+        return None
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is not on the current CUDA device")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
-def _head_rows(t, name, dtype=None):
-    """_rows of a [N, H, d] tensor whose heads are d apart."""
-    p = _rows(t, name, 3, dtype)
-    if t.shape[1] > 1 and t.stride(1) != t.shape[2]:
+def _rows_at(t, name, dtype, dev, shape, heads_apart=False):
+    """The same for a tensor whose last dimension alone has to be contiguous: (pointer, strides).
+    heads_apart: rows [N, H, d] whose heads follow one another."""
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is not on the current CUDA device")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] > 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    if heads_apart and st[1] != shape[2] and shape[1] > 1:
         raise ValueError(f"the heads of {name} must be contiguous")
-    return p
-
-
-def _shape(t, name, *shape):
-    if t is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {shape}")
-
-
-def _one_device(*tensors):
-    """All tensors (None aside) on the current device: the launch goes to its stream."""
-    cur = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.is_cuda and t.get_device() != cur:
-            raise ValueError(f"a tensor is on device {t.get_device()}, the current device is {cur}")
+    return t.data_ptr(), st
 
 
 def rope_table_scaled(method: str, theta: float, rd: int, max_len: int, factor: float = 1.0, orig_len: float = 0.0,
@@ -334,14 +341,16 @@ def rope_table_scaled(method: str, theta: float, rd: int, max_len: int, factor: 
 
 
 def _rope(fn, x, pos, rope_cs, out, layout, err_flag, stream):
-    N, H, d = x.shape
-    _shape(out, "out", N, H, d)
-    _shape(pos, "pos", N)
-    _shape(rope_cs, "rope_cs", rope_cs.shape[0], rope_cs.shape[1], 2)
-    _one_device(x, pos, rope_cs, out, err_flag)
-    _call(fn, _dt(x), _rows(x, "x", 3), x.stride(0), x.stride(1), N, H, d, _p(pos, torch.int32),
-          _p(rope_cs, torch.float32), rope_cs.shape[0], 2 * rope_cs.shape[1], int(layout),
-          _rows(out, "out", 3, x.dtype), out.stride(0), out.stride(1), _p(err_flag, torch.int32), _s(stream))
+    dt, dev = _dt(x), _dev()
+    N, H, d = shape = x.shape
+    xp, xs = _rows_at(x, "x", x.dtype, dev, shape)
+    op, os = _rows_at(out, "out", x.dtype, dev, shape)
+    max_len, half, two = rope_cs.shape
+    if two != 2:
+        raise ValueError("rope_cs must be [max_len, rd/2, 2]")
+    _call(fn, dt, xp, xs[0], xs[1], N, H, d, _at(pos, "pos", torch.int32, dev, (N,)),
+          _at(rope_cs, "rope_cs", torch.float32, dev), max_len, 2 * half, layout, op, os[0], os[1],
+          _at(err_flag, "err_flag", torch.int32, dev), _raw_stream(stream, dev))
 
 
 def rope(x, pos, rope_cs, out, layout=ROPE_HALF, err_flag=None, stream=None):
@@ -356,17 +365,20 @@ def rope_backward(dout, pos, rope_cs, dx, layout=ROPE_HALF, err_flag=None, strea
     _rope("msa_rope_backward", dout, pos, rope_cs, dx, layout, err_flag, stream)
 
 
-def _cache(Kpages, Vpages, block_table, seq_len, q_off, dtype):
-    """The cache arguments both paged entry points take, checked."""
-    kp, vp = _rows(Kpages, "Kpages", 4, dtype), _rows(Vpages, "Vpages", 4, dtype)
-    if Kpages.shape != Vpages.shape or Kpages.stride() != Vpages.stride():
-        raise ValueError("Kpages and Vpages must have the same shape and strides")
-    B = seq_len.numel()
-    _shape(q_off, "q_off", B + 1)
-    _shape(block_table, "block_table", B, block_table.shape[-1])
-    ps, rs, hs, _ = Kpages.stride()
-    return kp, vp, (Kpages.shape[0], Kpages.shape[1], ps, rs, hs, _p(block_table, torch.int32), block_table.shape[1],
-                    _p(seq_len, torch.int32))
+def _cache(Kpages, Vpages, block_table, seq_len, q_off, Hkv, d, dtype, dev):
+    """The batch and cache arguments both paged entry points take, checked: B, the pointer of
+    q_off, K, V and the rest in the order of the C signature."""
+    P, page = Kpages.shape[:2]
+    shape = (P, page, Hkv, d)
+    kp, ks = _rows_at(Kpages, "Kpages", dtype, dev, shape)
+    vp, vs = _rows_at(Vpages, "Vpages", dtype, dev, shape)
+    if ks != vs:
+        raise ValueError("Kpages and Vpages must have the same strides")
+    B, = seq_len.shape
+    max_pages = block_table.shape[-1]
+    return (B, _at(q_off, "q_off", torch.int64, dev, (B + 1,)), kp, vp, P, page, ks[0], ks[1], ks[2],
+            _at(block_table, "block_table", torch.int32, dev, (B, max_pages)), max_pages,
+            _at(seq_len, "seq_len", torch.int32, dev))
 
 
 def paged_append(q, k, v, q_off, seq_len, block_table, Kpages, Vpages, rope_cs=None, q_out=None, pos=None,
@@ -374,30 +386,26 @@ def paged_append(q, k, v, q_off, seq_len, block_table, Kpages, Vpages, rope_cs=N
     """New tokens into the paged cache (msa_paged_append): k (rotated) and v [N, Hkv, d] into the
     pages [num_pages, page, Hkv, d] (any strides) of their sequences, q (rotated) into q_out.
     q may be None; rope_cs None: no rotation; pos None: cache positions."""
+    dt, dev, dtype = _dt(k), _dev(), k.dtype
     N, Hkv, d = k.shape
-    _shape(v, "v", N, Hkv, d)
-    _shape(pos, "pos", N)
-    if tuple(Kpages.shape[2:]) != (Hkv, d):
-        raise ValueError("Kpages must be [num_pages, page, Hkv, d] of k's heads")
+    kp, ks = _rows_at(k, "k", dtype, dev, (N, Hkv, d), True)
+    vp, vs = _rows_at(v, "v", dtype, dev, (N, Hkv, d), True)
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
-    _one_device(q, k, v, q_off, seq_len, block_table, Kpages, Vpages, rope_cs, q_out, pos, err_flag)
-    qp = qop = None
-    Hq = qs = qos = 0
+    qp, qs, qop, qos, Hq = None, (0,), None, (0,), 0
     if q is not None:
         Hq = q.shape[1]
-        _shape(q, "q", N, Hq, d)
-        _shape(q_out, "q_out", N, Hq, d)
-        qp, qop, qs, qos = _head_rows(q, "q", k.dtype), _head_rows(q_out, "q_out", k.dtype), q.stride(0), q_out.stride(0)
-    max_len = rd = 0
+        qp, qs = _rows_at(q, "q", dtype, dev, (N, Hq, d), True)
+        qop, qos = _rows_at(q_out, "q_out", dtype, dev, (N, Hq, d), True)
+    max_len = half = 0
     if rope_cs is not None:
-        max_len, rd = rope_cs.shape[0], 2 * rope_cs.shape[1]
-        _shape(rope_cs, "rope_cs", max_len, rd // 2, 2)
-    kp, vp, cache = _cache(Kpages, Vpages, block_table, seq_len, q_off, k.dtype)
-    _call("msa_paged_append", _dt(k), qp, qs, qop, qos, Hq, _head_rows(k, "k"), k.stride(0),
-          _head_rows(v, "v", k.dtype), v.stride(0), N, seq_len.numel(), _p(q_off, torch.int64), Hkv, d,
-          _p(pos, torch.int32), _p(rope_cs, torch.float32), max_len, rd, int(layout), kp, vp, *cache,
-          _p(err_flag, torch.int32), _s(stream))
+        max_len, half, two = rope_cs.shape
+        if two != 2:
+            raise ValueError("rope_cs must be [max_len, rd/2, 2]")
+    B, qo, *cache = _cache(Kpages, Vpages, block_table, seq_len, q_off, Hkv, d, dtype, dev)
+    _call("msa_paged_append", dt, qp, qs[0], qop, qos[0], Hq, kp, ks[0], vp, vs[0], N, B, qo, Hkv, d,
+          _at(pos, "pos", torch.int32, dev, (N,)), _at(rope_cs, "rope_cs", torch.float32, dev), max_len, 2 * half,
+          layout, *cache, _at(err_flag, "err_flag", torch.int32, dev), _raw_stream(stream, dev))
 
 
 def paged_attn_workspace_size(dtype, B, max_q, Hq, Hkv, d, k=0, Mmax=0) -> int:
@@ -410,23 +418,22 @@ def paged_attn(Q, q_off, max_q, Kpages, Vpages, block_table, seq_len, O, ws, lse
     [N, Hq, d] packed by q_off int64 [B + 1] (at most max_q tokens a sequence), pages
     [num_pages, page, Hkv, d] (any strides), O [N, Hq, d], lse fp32 [Hq, N].  topk_idx int32 [B, k]
     with doc_chunk_off, Kbar and Vbar adds the selected documents' rows (at most Mmax)."""
-    N, Hq, d = Q.shape
+    dt, dev, dtype = _dt(Q), _dev(), Q.dtype
+    N, Hq, d = shape = Q.shape
     Hkv = Kpages.shape[2]
-    if Kpages.shape[-1] != d:
-        raise ValueError("Kpages must be [num_pages, page, Hkv, d] of Q's head size")
-    _shape(O, "O", N, Hq, d)
-    _shape(lse, "lse", Hq, N)
-    _one_device(Q, q_off, Kpages, Vpages, block_table, seq_len, O, ws, lse, topk_idx, doc_chunk_off, Kbar, Vbar,
-                err_flag)
-    B = seq_len.numel()
-    kp, vp, cache = _cache(Kpages, Vpages, block_table, seq_len, q_off, Q.dtype)
+    qp, qs = _rows_at(Q, "Q", dtype, dev, shape, True)
+    B, qo, *cache = _cache(Kpages, Vpages, block_table, seq_len, q_off, Hkv, d, dtype, dev)
+    idx = off = kb = vb = None
     k = D = C = 0
     if topk_idx is not None:
-        k, D, C = topk_idx.shape[1], doc_chunk_off.numel() - 1, Kbar.shape[0]
-        _shape(topk_idx, "topk_idx", B, k)
-        _shape(Kbar, "Kbar", C, Hkv, d)
-        _shape(Vbar, "Vbar", C, Hkv, d)
-    _call("msa_paged_attn", _dt(Q), _head_rows(Q, "Q"), Q.stride(0), N, B, max_q, _p(q_off, torch.int64), Hq, Hkv, d,
-          kp, vp, *cache, _p(topk_idx, torch.int32), k, _p(doc_chunk_off, torch.int64), D, C,
-          _p(Kbar, Q.dtype, host_ok=True), _p(Vbar, Q.dtype, host_ok=True), Mmax, float(scale), _p(O, Q.dtype),
-          _p(lse, torch.float32), _p(ws), ws.numel() * ws.element_size(), _p(err_flag, torch.int32), _s(stream))
+        if doc_chunk_off is None or Kbar is None or Vbar is None:
+            raise ValueError("topk_idx goes with doc_chunk_off, Kbar and Vbar")
+        k, D, C = topk_idx.shape[-1], doc_chunk_off.numel() - 1, Kbar.shape[0]
+        idx = _at(topk_idx, "topk_idx", torch.int32, dev, (B, k))
+        off = _at(doc_chunk_off, "doc_chunk_off", torch.int64, dev)
+        kb, vb = _at(Kbar, "Kbar", dtype, dev, (C, Hkv, d)), _at(Vbar, "Vbar", dtype, dev, (C, Hkv, d))
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("ws must be contiguous and on the current CUDA device")
+    _call("msa_paged_attn", dt, qp, qs[0], N, B, max_q, qo, Hq, Hkv, d, *cache, idx, k, off, D, C, kb, vb, Mmax, scale,
+          _at(O, "O", dtype, dev, shape), _at(lse, "lse", torch.float32, dev, (Hq, N)), ws.data_ptr(),
+          ws.numel() * ws.element_size(), _at(err_flag, "err_flag", torch.int32, dev), _raw_stream(stream, dev))

@@ -5,10 +5,10 @@
 // position (the cache position unless one is given).
 //
 // Bound by memory: q, k and v are read once, q_out and the cache rows written
-// once, all in 16-byte vectors; a thread takes one unit of the rotation (two
-// vectors) or one vector of v.  The token's place (its sequence by a warp-free
-// binary search over the offsets, one block-table entry) costs a few dependent
-// loads that overlap across the CTAs.
+// once.  A thread takes one unit (two 16-byte vectors) of up to four of the
+// token's heads (queries, keys, values in that order): their loads go out first,
+// and the token's place (its sequence, its block-table entry, the table's pairs: a
+// chain of dependent loads) is found while they are in flight.
 #include "common.cuh"
 #include "internal.h"
 #include "rope.cuh"
@@ -16,75 +16,91 @@
 namespace msa {
 namespace {
 
-template <typename T>
-__global__ void __launch_bounds__(256) paged_append_kernel(PagedAppendArgs a, int uq, int uk, int per_token,
-                                                           int64_t total) {
+template <typename T, bool kInter>
+__global__ void __launch_bounds__(256) paged_append_kernel(PagedAppendArgs a, int units, int groups, int64_t total) {
   pdl_wait();  // the offsets, lengths and projections may come from the previous kernel
   const PagedBatch& p = a.p;
-  const int Hkv = p.Hkv;
-  const int64_t step = (int64_t)gridDim.x * blockDim.x;
-  for (int64_t u = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; u < total; u += step) {
-    const int64_t n = u / per_token;
-    int e = (int)(u - n * per_token);
-    const bool report = e == 0;
-    // the last sequence whose offset is at or before n
-    int64_t lo = 0, hi = p.B;
+  const int Hkv = p.Hkv, Hq = a.q ? a.Hq : 0, heads = Hq + 2 * Hkv;
+  const int64_t id = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (id >= total) return;
+  const uint32_t per = (uint32_t)(units * groups);
+  const int64_t n = total < 0xffffffffll ? (int64_t)((uint32_t)id / per) : id / per;
+  const uint32_t r = (uint32_t)(id - n * per), hg = r / (uint32_t)units, u = r - hg * (uint32_t)units;
+  const bool report = r == 0;
+  const int rd = a.cs ? a.rd : 0;
+  const RopeUnit<T> rot((int)u, rd, kInter);  // of queries and keys
+  const int at1v = (int)u * 2 * Vec<T>::N + Vec<T>::N;
+  uint4 v0[kRopeHeads], v1[kRopeHeads];
+#pragma unroll
+  for (int j = 0; j < kRopeHeads; ++j) {
+    const int h = (int)hg + j * groups;
+    if (h < heads) {
+      const T* src;
+      if (h < Hq) src = reinterpret_cast<const T*>(a.q) + n * a.q_ts + h * a.d;
+      else if (h < Hq + Hkv) src = reinterpret_cast<const T*>(a.k) + n * a.k_ts + (h - Hq) * a.d;
+      else src = reinterpret_cast<const T*>(a.v) + n * a.v_ts + (h - Hq - Hkv) * a.d;
+      const bool val = h >= Hq + Hkv;
+      v0[j] = *reinterpret_cast<const uint4*>(src + (val ? at1v - Vec<T>::N : rot.at0));
+      v1[j] = *reinterpret_cast<const uint4*>(src + (val ? at1v : rot.at1));
+    }
+  }
+  // the last sequence whose offset is at or before n; the proportional guess is right for one
+  // token a sequence
+  int64_t lo = p.N < 0x7fffffff && p.B * n < 0x7fffffff ? (int64_t)((uint32_t)(p.B * n) / (uint32_t)p.N) : 0;
+  if (!(__ldg(p.q_off + lo) <= n && n < __ldg(p.q_off + lo + 1))) {
+    int64_t hi = p.B;
+    lo = 0;
     while (hi - lo > 1) {
       const int64_t mid = (lo + hi) >> 1;
       if (__ldg(p.q_off + mid) <= n) lo = mid; else hi = mid;
     }
-    const int64_t q0 = __ldg(p.q_off + lo), q1 = __ldg(p.q_off + lo + 1);
-    if (n < q0 || n >= q1) {  // a row behind the last sequence, or offsets that do not ascend from 0
-      if (report && n < q0) raise_flag(p.err_flag, MSA_FLAG_OFFSETS);
-      continue;
+  }
+  const int64_t q0 = __ldg(p.q_off + lo), q1 = __ldg(p.q_off + lo + 1);
+  if (n < q0 || n >= q1) {  // a row behind the last sequence, or offsets that do not ascend from 0
+    if (report && n < q0) raise_flag(p.err_flag, MSA_FLAG_OFFSETS);
+    return;
+  }
+  const int64_t at = (int64_t)__ldg(p.seq_len + lo) - (q1 - n);  // cache position
+  if (q1 > p.N || at < 0) {
+    if (report) raise_flag(p.err_flag, MSA_FLAG_OFFSETS);
+    return;
+  }
+  const uint32_t pi = (uint32_t)at / (uint32_t)p.page, row = (uint32_t)at - pi * (uint32_t)p.page;
+  const int64_t page = (int64_t)pi < p.max_pages ? __ldg(p.table + lo * p.max_pages + pi) : -1;
+  const int64_t rp = a.pos ? __ldg(a.pos + n) : at;  // rotary position
+  if (page < 0 || page >= p.num_pages || (a.cs && (rp < 0 || rp >= a.max_len))) {
+    if (report) raise_flag(p.err_flag, MSA_FLAG_INDEX_OOB);
+    return;
+  }
+  RopeTurn<T> turn;
+  if (rot.rotated) turn.load(a.cs + rp * rd, (int)u, 1.f);
+  const int64_t base = page * a.page_stride + row * a.row_stride;
+#pragma unroll
+  for (int j = 0; j < kRopeHeads; ++j) {
+    const int h = (int)hg + j * groups;
+    if (h < heads) {
+      const bool val = h >= Hq + Hkv;
+      T* dst;
+      if (h < Hq) dst = reinterpret_cast<T*>(a.q_out) + n * a.qo_ts + h * a.d;
+      else if (!val) dst = reinterpret_cast<T*>(a.K) + base + (h - Hq) * a.head_stride;
+      else dst = reinterpret_cast<T*>(a.V) + base + (h - Hq - Hkv) * a.head_stride;
+      if (rot.rotated && !val) turn.apply(v0[j], v1[j], kInter);
+      *reinterpret_cast<uint4*>(dst + (val ? at1v - Vec<T>::N : rot.at0)) = v0[j];
+      *reinterpret_cast<uint4*>(dst + (val ? at1v : rot.at1)) = v1[j];
     }
-    const int64_t len = __ldg(p.seq_len + lo);
-    const int64_t at = len - (q1 - n);  // cache position
-    if (q1 > p.N || at < 0) {
-      if (report) raise_flag(p.err_flag, MSA_FLAG_OFFSETS);
-      continue;
-    }
-    const int64_t pi = at / p.page;
-    const int row = (int)(at - pi * p.page);
-    const int64_t page = pi < p.max_pages ? __ldg(p.table + lo * p.max_pages + pi) : -1;
-    const int64_t rp = a.pos ? __ldg(a.pos + n) : at;  // rotary position
-    if (page < 0 || page >= p.num_pages || (a.cs && (rp < 0 || rp >= a.max_len))) {
-      if (report) raise_flag(p.err_flag, MSA_FLAG_INDEX_OOB);
-      continue;
-    }
-    const float* cs = a.cs ? a.cs + rp * a.rd : nullptr;
-    const int rd = a.cs ? a.rd : 0;
-    const int64_t base = page * a.page_stride + row * a.row_stride;
-    if (e < Hkv * uk) {
-      const int h = e / uk;
-      rotate_unit<T>(reinterpret_cast<const T*>(a.k) + n * a.k_ts + h * a.d,
-                     reinterpret_cast<T*>(a.K) + base + h * a.head_stride, e - h * uk, rd, a.interleaved, false, cs);
-      continue;
-    }
-    e -= Hkv * uk;
-    const int uv = a.d / Vec<T>::N;
-    if (e < Hkv * uv) {
-      const int h = e / uv, c = (e - h * uv) * Vec<T>::N;
-      *reinterpret_cast<uint4*>(reinterpret_cast<T*>(a.V) + base + h * a.head_stride + c) =
-          *reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.v) + n * a.v_ts + h * a.d + c);
-      continue;
-    }
-    e -= Hkv * uv;
-    const int h = e / uq;
-    rotate_unit<T>(reinterpret_cast<const T*>(a.q) + n * a.q_ts + h * a.d,
-                   reinterpret_cast<T*>(a.q_out) + n * a.qo_ts + h * a.d, e - h * uq, rd, a.interleaved, false, cs);
   }
 }
 
 template <typename T>
 cudaError_t append_t(const PagedAppendArgs& a, cudaStream_t s) {
-  const int unit = rope_units<T>(a.d, a.cs ? a.rd : 0, a.interleaved);
-  const int per_token = a.p.Hkv * (unit + a.d / Vec<T>::N) + (a.q ? a.Hq * unit : 0);
-  const int64_t total = a.p.N * per_token;
+  const int units = RopeUnit<T>::per_head(a.d);
+  const int groups = ((a.q ? a.Hq : 0) + 2 * a.p.Hkv + kRopeHeads - 1) / kRopeHeads;
+  const int64_t total = a.p.N * units * groups;
   const int64_t blocks = (total + 255) / 256;
-  const unsigned grid = (unsigned)(blocks < 0x7fffffff ? blocks : 0x7fffffff);
+  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;  // grid x
   count_launch();
-  return launch_pdl(paged_append_kernel<T>, dim3(grid), dim3(256), 0, s, a, unit, unit, per_token, total);
+  return launch_pdl(a.interleaved ? paged_append_kernel<T, true> : paged_append_kernel<T, false>,
+                    dim3((unsigned)blocks), dim3(256), 0, s, a, units, groups, total);
 }
 
 }  // namespace

@@ -51,13 +51,13 @@ __global__ void __launch_bounds__(kF32Threads) paged_f32_kernel(PagedAttnArgs a,
   const int G = a.Hq / p.Hkv;
   pdl_wait();
   find_start(p, TB, blockIdx.x, gridDim.x, blockIdx.x == 0, &sm.st);
-  if (tid == 0) leave_mark(&sm.st, marks + blockIdx.x);
+  if (tid == 0) leave_mark(&sm.st, TB, blockIdx.x, marks + blockIdx.x);
   pdl_trigger();
   if (!sm.st.any) return;
   const float sl2 = a.scale * 1.4426950408889634f;
   const float* Q = reinterpret_cast<const float*>(a.Q);
 
-  for (Walk w(p, TB, &sm.st); w.more(); w.next(p, TB)) {
+  for (Walk w(TB, &sm.st); w.more(); w.next(p, TB)) {
     const Seq& s = w.s;
     const int tb0 = w.i * TB;
     __syncthreads();  // the previous segment's readers are done
@@ -209,64 +209,74 @@ __global__ void __launch_bounds__(kF32Threads) paged_f32_kernel(PagedAttnArgs a,
 }
 
 // O = sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s over an item's segments, in the
-// order of the CTAs.  Block x merges the item that border x + 1 is the first to cut
-// (if there is one); block y takes 32 of its rows, a thread four values of a row.
+// order of the CTAs.  Block x merges the item of mark x + 1, if there is one; block y
+// takes kMergeRows of its rows, a thread four values of a row.  A chain of dependent
+// loads (mark, maxima, values) bounds it, so few rows per block: all are in flight.
+constexpr int kMergeRows = 8;
 template <typename T, int DH, bool kQuads>
-__global__ void __launch_bounds__(256) merge_kernel(MergeArgs a) {
+__global__ void __launch_bounds__(kMergeRows * (DH / 4)) merge_kernel(MergeArgs a) {
   pdl_wait();
   const int64_t c = (int64_t)blockIdx.x + 1;
   const Mark mk = a.marks[c];
-  if (!mk.any || mk.t == 0) return;
-  const Seq s = load_seq(a.p, mk.b);
-  const int64_t start = mk.f0 - mk.t, per = mk.per;
-  const int64_t c0 = start / per, c1 = (start + block_tiles(s, a.TB, mk.i) - 1) / per;
-  if (c0 != c - 1) return;  // an earlier border's block merges this item
-  const int quad = threadIdx.x >> 3;
-  if (quad >= DH / 4) return;
+  // consecutive threads: rows first in the quads layout, values of a row first in the other
+  const int quad = kQuads ? threadIdx.x / kMergeRows : threadIdx.x % (DH / 4);
+  const int r = blockIdx.y * kMergeRows + (kQuads ? threadIdx.x % kMergeRows : threadIdx.x / (DH / 4));
+  const int tl = r / a.G, hh = r - tl * a.G;
+  if (tl >= mk.tokens) return;
   const size_t sf = slot_floats(a.rows, DH);
-  const bool late = start != c0 * per;  // the first segment is its CTA's last one, not its first
-#pragma unroll 1
-  for (int j = 0; j < 4; ++j) {
-    const int r = blockIdx.y * 32 + j * 8 + (threadIdx.x & 7);
-    const int t = mk.i * a.TB + r / a.G;
-    if (r >= a.TB * a.G || t >= s.nq) continue;
-    auto slot = [&](int64_t x) { return a.slots + (2 * x + (x == c0 && late ? 1 : 0)) * sf; };
-    float m = -INFINITY;
-#pragma unroll 4
-    for (int64_t x = c0; x <= c1; ++x) m = fmaxf(m, __ldg(slot(x) + a.rows * DH + 2 * r));
-    float l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int64_t x = c0; x <= c1; ++x) {
-      const float* src = slot(x);
-      const float2 ml = __ldg(reinterpret_cast<const float2*>(src + a.rows * DH + 2 * r));
-      const float4 v = __ldg(reinterpret_cast<const float4*>(src + (kQuads ? (quad * a.rows + r) * 4 : r * DH + quad * 4)));
-      const float w = ml.y == 0.f ? 0.f : exp2f((ml.x - m) * a.unit_log2);  // sum 0: no key was visible
-      l += w * ml.y;
-      acc[0] += w * v.x;
-      acc[1] += w * v.y;
-      acc[2] += w * v.z;
-      acc[3] += w * v.w;
+  const float* first = a.slots + (2 * mk.c0 + mk.late) * sf;
+  const float* rest = a.slots + 2 * mk.c0 * sf;  // segment x > 0 is in slot 2 (c0 + x)
+  const int ml_at = a.rows * DH + 2 * r, v_at = kQuads ? (quad * a.rows + r) * 4 : r * DH + quad * 4;
+  float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int x0 = 0; x0 < mk.n; x0 += 4) {
+    float2 ml[4];
+    float4 v[4];
+    float top = m;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (x0 + j >= mk.n) continue;
+      const float* src = x0 + j == 0 ? first : rest + 2 * (size_t)(x0 + j) * sf;
+      ml[j] = *reinterpret_cast<const float2*>(src + ml_at);
+      v[j] = *reinterpret_cast<const float4*>(src + v_at);
     }
-    const bool seen = l != 0.f;
-    const float inv = seen ? 1.f / l : 0.f;
-    const int h = mk.g * a.G + r % a.G;
-    T* dst = reinterpret_cast<T*>(a.O) + ((s.q0 + t) * a.Hq + h) * DH + quad * 4;
-    if constexpr (sizeof(T) == 4)
-      *reinterpret_cast<float4*>(dst) = make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
-    else
-      *reinterpret_cast<uint2*>(dst) =
-          make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
-    if (a.lse && quad == 0)
-      a.lse[(int64_t)h * a.p.N + s.q0 + t] =
-          seen ? (m * a.unit_log2 + log2f(l)) * 0.69314718055994531f : -INFINITY;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (x0 + j < mk.n) top = fmaxf(top, ml[j].x);
+    const float corr = l == 0.f ? 0.f : exp2f((m - top) * a.unit_log2);
+    l *= corr;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] *= corr;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (x0 + j >= mk.n) continue;
+      const float w = ml[j].y == 0.f ? 0.f : exp2f((ml[j].x - top) * a.unit_log2);  // sum 0: no key was visible
+      l += w * ml[j].y;
+      acc[0] += w * v[j].x;
+      acc[1] += w * v[j].y;
+      acc[2] += w * v[j].z;
+      acc[3] += w * v[j].w;
+    }
+    m = top;
   }
+  const bool seen = l != 0.f;
+  const float inv = seen ? 1.f / l : 0.f;
+  const int64_t row = mk.row + tl;
+  const int h = mk.g * a.G + hh;
+  T* dst = reinterpret_cast<T*>(a.O) + (row * a.Hq + h) * DH + quad * 4;
+  if constexpr (sizeof(T) == 4)
+    *reinterpret_cast<float4*>(dst) = make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
+  else
+    *reinterpret_cast<uint2*>(dst) =
+        make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+  if (a.lse && quad == 0)
+    a.lse[(int64_t)h * a.N + row] = seen ? (m * a.unit_log2 + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
 template <int DH, int RPT>
 cudaError_t f32_t(const PagedAttnArgs& a, int TB, cudaStream_t s) {
   using S = F32Smem<DH, RPT>;
-  cudaError_t e = cudaFuncSetAttribute(paged_f32_kernel<DH, RPT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)sizeof(S));
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(paged_f32_kernel<DH, RPT>, (int)sizeof(S), done);
   if (e != cudaSuccess) return e;
   const int grid = 2 * sm_count();
   Mark* marks = reinterpret_cast<Mark*>(a.part);
@@ -274,7 +284,7 @@ cudaError_t f32_t(const PagedAttnArgs& a, int TB, cudaStream_t s) {
   count_launch();
   e = launch_pdl(paged_f32_kernel<DH, RPT>, dim3((unsigned)grid), dim3(kF32Threads), sizeof(S), s, a, TB, marks, slots);
   if (e != cudaSuccess) return e;
-  MergeArgs m{a.p, marks, slots, S::RB, TB, a.Hq / a.p.Hkv, a.Hq, a.scale * 1.4426950408889634f, a.O, a.lse};
+  MergeArgs m{marks, slots, a.p.N, S::RB, a.Hq / a.p.Hkv, a.Hq, a.scale * 1.4426950408889634f, a.O, a.lse};
   return launch_merge(MSA_F32, DH, false, m, grid, s);
 }
 
@@ -285,13 +295,13 @@ bool few_rows(int Hq, int Hkv, int max_q) { return (int64_t)(Hq / Hkv) * max_q <
 
 cudaError_t launch_merge(msa_dtype dt, int d, bool quads, const MergeArgs& a, int grid, cudaStream_t s) {
   if (grid < 2) return cudaSuccess;
-  const dim3 g((unsigned)(grid - 1), (unsigned)((a.rows + 31) / 32));
+  const dim3 g((unsigned)(grid - 1), (unsigned)((a.rows + kMergeRows - 1) / kMergeRows));
+  const dim3 t((unsigned)(kMergeRows * (d / 4)));
+  auto k = dt == MSA_F32 ? (d == 64 ? merge_kernel<float, 64, false> : merge_kernel<float, 128, false>)
+           : !quads      ? merge_kernel<__nv_bfloat16, 128, false>
+                         : (d == 64 ? merge_kernel<__nv_bfloat16, 64, true> : merge_kernel<__nv_bfloat16, 128, true>);
   count_launch();
-  if (dt == MSA_F32) return launch_pdl(d == 64 ? merge_kernel<float, 64, false> : merge_kernel<float, 128, false>, g, dim3(256), 0, s, a);
-  if (quads)
-    return launch_pdl(d == 64 ? merge_kernel<__nv_bfloat16, 64, true> : merge_kernel<__nv_bfloat16, 128, true>, g,
-                      dim3(256), 0, s, a);
-  return launch_pdl(merge_kernel<__nv_bfloat16, 128, false>, g, dim3(256), 0, s, a);
+  return launch_pdl(k, g, t, 0, s, a);
 }
 
 }  // namespace paged

@@ -63,7 +63,7 @@ struct DLayout {
   static constexpr int kStage = 2 * kTile;
   static constexpr int kQ = kMaxRows * kDH * 2;       // Q rows, K-major, 128-byte swizzle (two buffers)
   static constexpr int kP = kMaxRows * kKeys * 2;     // P^T rows (query rows x keys); two buffers
-  static constexpr int kRed = 3 * kMaxRows * 4 * 4;    // [2 tile parities + segment end][rows][4 warps]
+  static constexpr int kRed = 2 * kMaxRows * 4 * 4;    // [maxima, sums][rows][4 warps]
   static constexpr int kSmem = 1024 + kStages * kStage + 2 * kQ + 2 * kP + kRed + 8 * 18 + (int)sizeof(Start);
   static_assert(kSmem <= 232448, "shared memory of one CTA");
   static constexpr uint32_t kTmemCols = 64;           // S0, S1, O (16 columns each)
@@ -75,6 +75,15 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 __device__ __forceinline__ void bar_softmax() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// Whether v holds in any of the 128 softmax threads (a barrier among them).
+__device__ __forceinline__ bool any_softmax(bool v) {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %1, 0;\n bar.red.popc.u32 %0, 1, 128, p;\n}"
+               : "=r"(r)
+               : "r"((uint32_t)v)
+               : "memory");
+  return r != 0;
+}
 // Maximum of v over the 32 lanes, in every lane (one instruction on sm_100a).
 __device__ __forceinline__ float warp_max(float v) {
   float r;
@@ -101,7 +110,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmKm, const __grid_const
   uint8_t* ring = smem;
   uint8_t* Qs = ring + kStages * DLayout::kStage;  // two buffers, alternating by segment
   uint8_t* Ps = Qs + 2 * DLayout::kQ;
-  float* red_s = reinterpret_cast<float*>(Ps + 2 * DLayout::kP);  // [3][16 rows][4 warps]
+  float* red_s = reinterpret_cast<float*>(Ps + 2 * DLayout::kP);  // [2][16 rows][4 warps]
   uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(red_s) + DLayout::kRed);
   uint64_t* kv_full = bars;            // [3]
   uint64_t* kv_empty = bars + 3;       // [3]
@@ -139,7 +148,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmKm, const __grid_const
   // a programmatic dependent: nothing an earlier kernel writes is read before this wait
   pdl_wait();
   find_start(p, TB, blockIdx.x, gridDim.x, blockIdx.x == 0, start);
-  if (tid == 0) leave_mark(start, a.marks + blockIdx.x);
+  if (tid == 0) leave_mark(start, TB, blockIdx.x, a.marks + blockIdx.x);
   pdl_trigger();
   if (!start->any) return;
   if (warp == 1) {
@@ -160,7 +169,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmKm, const __grid_const
     // swizzle atom, so the tile's layout is that of one 128-row box.
     uint32_t it = 0;
     bool stop = false;
-    for (Walk w(p, TB, start); w.more() && !stop; w.next(p, TB)) {
+    for (Walk w(TB, start); w.more() && !stop; w.next(p, TB)) {
       for (int t = w.t0; t < w.t0 + w.n; ++t, ++it) {
         const uint32_t st = it % kStages, round = it / kStages;
         const bool mem = t < w.s.nm;
@@ -226,7 +235,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmKm, const __grid_const
       constexpr uint32_t idO = idesc_bf16_f32(kDH, kMaxRows, /*b_mn=*/false, /*a_mn=*/true);  // V^T x P^T
       const uint32_t p0 = smem_u32(Ps);
       uint32_t it = 0, nseg = 0;  // it: tiles (K/V stages, S and P buffers); nseg: segments
-      for (Walk w(p, TB, start); w.more() && !*abort_s; w.next(p, TB), ++nseg) {
+      for (Walk w(TB, start); w.more() && !*abort_s; w.next(p, TB), ++nseg) {
         const int T = w.n;
         const uint32_t q0 = smem_u32(Qs + (nseg & 1) * DLayout::kQ);
         if (!mbar_wait_or_stop(q_ready, nseg & 1, kWaitPolls, abort_s)) break;
@@ -305,7 +314,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmKm, const __grid_const
         *reinterpret_cast<uint4*>(buf + sw128_off(r, c8, kMaxRows)) = v[k];
       }
     };
-    Walk w(p, TB, start);
+    Walk w(TB, start);
     {
       uint4 v[2];
       load_q(w, v);
@@ -353,12 +362,11 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmKm, const __grid_const
         mbar_arrive(&s_free[sb]);
         // mask; scale into the log2 domain
         const int key = (t - w.s.nm) * kKeys + r_lane;  // cache position of a local key
-        const bool mem_vis = (r_lane & (kSegRows - 1)) < seg_n;
+        // rows from `low` on see the key: token r / G >= key - pos0 means r >= (key - pos0) G
+        const int low = mem ? ((r_lane & (kSegRows - 1)) < seg_n ? 0 : kR)
+                            : (key < pos0 ? 0 : min(key - pos0, kR) * a.G);
 #pragma unroll
-        for (int r = 0; r < kR; ++r) {
-          const bool vis = r < rows && (mem ? mem_vis : key <= pos0 + r / a.G);
-          sc[r] = vis ? sc[r] * a.scale_log2 : -INFINITY;
-        }
+        for (int r = 0; r < kR; ++r) sc[r] = r >= low && r < rows ? sc[r] * a.scale_log2 : -INFINITY;
         // Rows of V past the sequence's end: zeros (see above).  The copy that filled the
         // stage has landed (S read the same barrier's K); this wait makes it visible here.
         if (!mem && w.s.len - (key - r_lane) < kKeys) {
@@ -372,31 +380,33 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmKm, const __grid_const
           }
           __syncwarp();
         }
-        // column maxima over the tile's 128 keys: a warp reduction per column,
-        // then the four warps' maxima through shared memory.  The exchange
-        // buffer alternates with the tile's parity, so one barrier per tile
-        // suffices (a buffer is rewritten two tiles later, after every thread
-        // has passed the barrier of the tile in between).
-        float* red = red_s + (g & 1) * (kMaxRows * 4);
-        float mine = -INFINITY;  // lane r < kR keeps this warp's maximum of column r
+        // The maximum moves only where a score passes it by 2^8 (always in the first tile with a
+        // visible key): one vote over the 128 keys, and the column maxima (a warp reduction per
+        // column, then the four warps' through shared memory) only if it says so.
+        bool over = false;
 #pragma unroll
-        for (int r = 0; r < kR; ++r) {
-          const float v = warp_max(sc[r]);
-          mine = lane == r ? v : mine;
-        }
-        if (lane < kR) red[lane * 4 + q] = mine;
-        bar_softmax();
-        bool grow = false;
+        for (int r = 0; r < kR; ++r) over |= sc[r] > m_run[r] + kRescaleLog2;
+        const bool grow = any_softmax(over);
         float corr[kR];
 #pragma unroll
-        for (int r = 0; r < kR; ++r) {
-          const float4 wv = *reinterpret_cast<const float4*>(red + r * 4);
-          const float mt = fmaxf(fmaxf(wv.x, wv.y), fmaxf(wv.z, wv.w));
-          corr[r] = 1.f;
-          if (mt > m_run[r] + kRescaleLog2) {  // same decision in every thread
-            corr[r] = m_run[r] == -INFINITY ? 0.f : fast_exp2(m_run[r] - mt);
-            m_run[r] = mt;
-            grow = true;
+        for (int r = 0; r < kR; ++r) corr[r] = 1.f;
+        if (grow) {
+          float mine = -INFINITY;  // lane r < kR keeps this warp's maximum of column r
+#pragma unroll
+          for (int r = 0; r < kR; ++r) {
+            const float v = warp_max(sc[r]);
+            mine = lane == r ? v : mine;
+          }
+          if (lane < kR) red_s[lane * 4 + q] = mine;
+          bar_softmax();
+#pragma unroll
+          for (int r = 0; r < kR; ++r) {
+            const float4 wv = *reinterpret_cast<const float4*>(red_s + r * 4);
+            const float mt = fmaxf(fmaxf(wv.x, wv.y), fmaxf(wv.z, wv.w));
+            if (mt > m_run[r] + kRescaleLog2) {  // same decision in every thread
+              corr[r] = m_run[r] == -INFINITY ? 0.f : fast_exp2(m_run[r] - mt);
+              m_run[r] = mt;
+            }
           }
         }
         float pr[kR];
@@ -441,7 +451,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmKm, const __grid_const
       float o[kR];
       tmem_ld_cols<kR>(tO + lane_off, o);
       tmem_ld_wait();
-      float* red_l = red_s + 2 * (kMaxRows * 4);  // the segment's row sums, apart from the tile buffers
+      float* red_l = red_s + kMaxRows * 4;  // the segment's row sums, apart from the maxima
 #pragma unroll
       for (int r = 0; r < kR; ++r) {
         float v = l_run[r];
@@ -522,12 +532,13 @@ cudaError_t launch_paged_decode(const PagedAttnArgs& a, cudaStream_t s) {
   d.slots = reinterpret_cast<float*>(reinterpret_cast<char*>(a.part) + marks_bytes(grid));
   d.scale_log2 = a.scale * 1.4426950408889634f;
   auto kern = d.R <= 4 ? paged_decode_kernel<4> : (d.R <= 8 ? paged_decode_kernel<8> : paged_decode_kernel<16>);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, DLayout::kSmem);
+  static std::atomic<uint64_t> done[3];
+  cudaError_t e = allow_smem(kern, DLayout::kSmem, done[d.R <= 4 ? 0 : (d.R <= 8 ? 1 : 2)]);
   if (e != cudaSuccess) return e;
   count_launch();
   e = launch_pdl(kern, dim3((unsigned)grid), dim3(kThreads), (size_t)DLayout::kSmem, s, tkm, tvm, tkl, tvl, d);
   if (e != cudaSuccess) return e;
-  MergeArgs m{a.p, d.marks, d.slots, d.R, a.p.max_q, G, a.Hq, 1.f, a.O, a.lse};
+  MergeArgs m{d.marks, d.slots, a.p.N, d.R, G, a.Hq, 1.f, a.O, a.lse};
   return launch_merge(MSA_BF16, kDH, false, m, grid, s);
 }
 

@@ -189,7 +189,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmKm, const __grid_cons
   // a programmatic dependent: nothing an earlier kernel writes is read before this wait
   pdl_wait();
   find_start(p, TB, blockIdx.x, gridDim.x, blockIdx.x == 0, start);
-  if (threadIdx.x == 0) leave_mark(start, a.marks + blockIdx.x);
+  if (threadIdx.x == 0) leave_mark(start, TB, blockIdx.x, a.marks + blockIdx.x);
   pdl_trigger();
   if (!start->any) return;
   if (warp == 1) {
@@ -212,7 +212,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmKm, const __grid_cons
     // swizzle atom, so the tile's layout is that of one 128-row box.
     uint32_t it = 0;
     bool stop = false;
-    for (Walk w(p, TB, start); w.more() && !stop; w.next(p, TB)) {
+    for (Walk w(TB, start); w.more() && !stop; w.next(p, TB)) {
       for (int t = w.t0; t < w.t0 + w.n; ++t, ++it) {
         const uint32_t st = it % kKV, round = it / kKV;
         const bool mem = t < w.s.nm;
@@ -277,7 +277,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmKm, const __grid_cons
       const uint64_t dk0 = desc_k_sw128(smem_u32(Ks));
       uint32_t g = 0, nseg = 0;
       bool ok = true;
-      for (Walk w(p, TB, start); ok && w.more(); w.next(p, TB), ++nseg) {
+      for (Walk w(TB, start); ok && w.more(); w.next(p, TB), ++nseg) {
         const uint32_t tQ = tQ0 + (nseg & 1) * (DH / 2);
         ok = wait(q_tmem, nseg & 1);
         for (int j = 0; ok && j < w.n; ++j, ++g) {
@@ -307,7 +307,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmKm, const __grid_cons
       const uint64_t dv0 = desc_mn_sw128(smem_u32(Vs), kKeys * 128);
       uint32_t g = 0;
       bool ok = true;
-      for (Walk w(p, TB, start); ok && w.more(); w.next(p, TB)) {
+      for (Walk w(TB, start); ok && w.more(); w.next(p, TB)) {
         for (int j = 0; ok && j < w.n; ++j, ++g) {
           const uint32_t st = g & 1, vs = g % kKV;
           // P written over S; V landed with K
@@ -368,7 +368,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmKm, const __grid_cons
       tc_fence_before();
       mbar_arrive(q_tmem);
     };
-    Walk w(p, TB, start);
+    Walk w(TB, start);
     fetch_q(w);
     place_q(tQ0);
     uint32_t g = 0, nseg = 0;
@@ -607,14 +607,14 @@ cudaError_t prefill_t(const PagedAttnArgs& a, cudaStream_t s) {
   d.marks = reinterpret_cast<Mark*>(a.part);
   d.slots = reinterpret_cast<float*>(reinterpret_cast<char*>(a.part) + marks_bytes(grid));
   d.scale_log2 = a.scale * 1.4426950408889634f;
-  cudaError_t e =
-      cudaFuncSetAttribute(paged_prefill_kernel<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(paged_prefill_kernel<DH>, L::kSmem, done);
   if (e != cudaSuccess) return e;
   count_launch();
   e = launch_pdl(paged_prefill_kernel<DH>, dim3((unsigned)grid), dim3(kThreads), (size_t)L::kSmem, s, tkm, tvm, tkl,
                  tvl, d);
   if (e != cudaSuccess) return e;
-  MergeArgs m{a.p, d.marks, d.slots, kRows, d.TB, G, a.Hq, 1.f, a.O, a.lse};
+  MergeArgs m{d.marks, d.slots, a.p.N, kRows, G, a.Hq, 1.f, a.O, a.lse};
   return launch_merge(MSA_BF16, DH, true, m, grid, s);
 }
 

@@ -61,19 +61,31 @@ __device__ __forceinline__ int block_tiles(const Seq& s, int TB, int i) {
   return max(1, s.nm + lt);
 }
 
-// sum over 0 <= i < n of floor((a i + b) / m), for a, b >= 0 and m > 0, by the
-// Euclidean reduction of (a, m) (the lattice points under a line).
-__device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+// sum over 0 <= i < n of floor((a i + b) / 128), a >= 1, b >= 0, a n + b < 2^32.
+// For a power of two a <= 128 the quotients repeat c = 128 / a times each; else
+// by the Euclidean reduction of (a, 128) (the lattice points under a line).
+__device__ __forceinline__ int64_t sum_div_keys(uint32_t n, uint32_t a, uint32_t b) {
+  static_assert(kKeys == 128, "shifts by 7");
+  if ((a & (a - 1)) == 0 && a <= 128u) {
+    const int sh = 7 - (31 - __clz(a));  // log2(128 / a)
+    auto upto = [&](uint32_t x) {        // sum over j < x of j >> sh
+      const int64_t q = x >> sh, r = x & ((1u << sh) - 1);
+      return ((q * (q - 1)) >> 1 << sh) + q * r;
+    };
+    const uint32_t x0 = b / a;
+    return upto(x0 + n) - upto(x0);
+  }
   int64_t ans = 0;
+  uint32_t m = 128;
   while (n > 0) {
-    ans += n * (n - 1) / 2 * (a / m) + n * (b / m);
+    ans += (int64_t)n * (n - 1) / 2 * (a / m) + (int64_t)n * (b / m);
     a %= m;
     b %= m;
-    const int64_t y = a * n + b;
+    const uint32_t y = a * n + b;
     if (y < m) break;
     n = y / m;
     b = y % m;
-    const int64_t t = a;
+    const uint32_t t = a;
     a = m;
     m = t;
   }
@@ -82,36 +94,43 @@ __device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, in
 
 // Tiles of blocks [0, n) of a sequence.
 __device__ __forceinline__ int64_t tiles_before(const Seq& s, int TB, int n) {
-  const int nb = (s.nq + TB - 1) / TB;
+  const int nb = (int)(((uint32_t)s.nq + TB - 1) / (uint32_t)TB);
   if (nb == 0 || n <= 0) return 0;
   const bool all = n >= nb;
-  const int64_t m = all ? nb - 1 : n;  // blocks of TB whole tokens
-  const int64_t hist = (int64_t)s.len - s.nq;
-  int64_t i0 = hist >= 0 ? 0 : -hist / TB;  // blocks that end at or before position 0 see no local key
-  if (i0 > m) i0 = m;
-  int64_t t = i0 * max(1, s.nm);
-  if (m > i0) t += (m - i0) * s.nm + floor_sum(m - i0, kKeys, TB, hist + (i0 + 1) * TB + kKeys - 1);
+  const int m = all ? nb - 1 : n;  // blocks of TB whole tokens
+  int64_t t = 0;
+  if (m > 0) {
+    const int hist = s.len - s.nq;
+    // blocks that end at or before position 0 see no local key
+    const int i0 = hist >= 0 ? 0 : min(m, -hist / TB);
+    t = (int64_t)i0 * max(1, s.nm);
+    if (m > i0)
+      t += (int64_t)(m - i0) * s.nm + sum_div_keys(m - i0, TB, (uint32_t)hist + (uint32_t)((i0 + 1) * TB) + kKeys - 1);
+  }
   return all ? t + block_tiles(s, TB, nb - 1) : t;
 }
 
 struct Start {            // where a CTA's share begins
   int64_t per, f0, f1;    // tiles per CTA, the share
   int64_t b;              // sequence, KV head, block and tile of f0
+  Seq s;
   int g, i, t;
   int any;                // the share is not empty
-  int64_t sums[32];       // scan scratch (one per warp)
+  int64_t rest;           // scan scratch: tile of the sequence, sums per warp
+  int64_t sums[16];
 };
 
-// All threads of the CTA call it (blockDim.x a multiple of 32, at most 1024);
+// All threads of the CTA call it (blockDim.x a multiple of 32, at most 512);
 // on return st (shared memory) holds share c of `grid` shares.
 __device__ __forceinline__ void find_start(const PagedBatch& p, int TB, int64_t c, int64_t grid, bool report,
                                            Start* st) {
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t chunk = (p.B + nt - 1) / nt;
-  const int64_t b0 = min(p.B, tid * chunk), b1 = min(p.B, b0 + chunk);
+  const int chunk = (int)((p.B + nt - 1) / nt);  // B < 2^31
+  const int64_t b0 = min(p.B, (int64_t)tid * chunk), b1 = min(p.B, b0 + chunk);
   int64_t mine = 0;
+  Seq s;
   for (int64_t b = b0; b < b1; ++b) {
-    const Seq s = load_seq(p, b, report ? p.err_flag : nullptr);
+    s = load_seq(p, b, report ? p.err_flag : nullptr);
     mine += tiles_before(s, TB, 0x7fffffff);
   }
   int64_t incl = mine;
@@ -129,34 +148,53 @@ __device__ __forceinline__ void find_start(const PagedBatch& p, int TB, int64_t 
   }
   incl += before;
   const int64_t Ttot = total * p.Hkv;
-  const int64_t per = max((int64_t)1, (Ttot + grid - 1) / grid);
+  // 32-bit divisions where the numbers allow (64-bit ones cost about a microsecond together)
+  const bool small = Ttot + grid < 0x7fffffff;
+  const int64_t per = max((int64_t)1, small ? (int64_t)((uint32_t)(Ttot + grid - 1) / (uint32_t)grid)
+                                            : (Ttot + grid - 1) / grid);
   const int64_t f0 = c * per, f1 = min(f0 + per, Ttot);
+  const bool any = f0 < f1;
+  const int64_t g = !any ? 0 : small ? (int64_t)((uint32_t)f0 / (uint32_t)total) : f0 / total;
   if (tid == 0) {
     st->per = per;
     st->f0 = f0;
     st->f1 = f1;
-    st->any = f0 < f1;
+    st->any = any;
+    st->g = (int)g;
   }
-  if (f0 < f1) {
-    const int64_t g = f0 / total, w = f0 - g * total;
-    if (w >= incl - mine && w < incl) {  // exactly one thread
-      int64_t rest = w - (incl - mine), b = b0;
-      Seq s = load_seq(p, b);
+  const int64_t w = f0 - g * total;
+  if (any && w >= incl - mine && w < incl) {  // exactly one thread
+    int64_t rest = w - (incl - mine), b = b0;
+    if (chunk > 1) {
       for (;;) {
+        s = load_seq(p, b);
         const int64_t n = tiles_before(s, TB, 0x7fffffff);
         if (rest < n) break;
         rest -= n;
-        s = load_seq(p, ++b);
+        ++b;
       }
-      int lo = 0, hi = (s.nq + TB - 1) / TB;  // the block holding tile `rest`: tiles_before(lo) <= rest
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (tiles_before(s, TB, mid) <= rest) lo = mid; else hi = mid;
-      }
-      st->b = b;
-      st->g = (int)g;
+    }
+    st->b = b;
+    st->s = s;
+    st->rest = rest;
+  }
+  __syncthreads();
+  if (any && warp == 0) {
+    // the block holding tile `rest`: the last one with tiles_before(block) <= rest, 32 probes at a time
+    const Seq q = st->s;
+    const int64_t rest = st->rest;
+    int lo = 0, n = (int)(((uint32_t)q.nq + TB - 1) / (uint32_t)TB);  // answer in [lo, lo + n)
+    while (n > 1) {
+      const int step = (n + 31) >> 5;
+      const int at = lo + lane * step;
+      const unsigned hit = __ballot_sync(0xffffffffu, lane * step < n && tiles_before(q, TB, at) <= rest);
+      const int last = 31 - __clz(hit);  // lane 0 always hits
+      lo += last * step;
+      n = min(step, n - last * step);
+    }
+    if (lane == 0) {
       st->i = lo;
-      st->t = (int)(rest - tiles_before(s, TB, lo));
+      st->t = (int)(rest - tiles_before(q, TB, lo));
     }
   }
   __syncthreads();
@@ -171,9 +209,8 @@ struct Walk {
     T = block_tiles(s, TB, i);
     n = (int)min((int64_t)(T - t0), f1 - f);
   }
-  __device__ __forceinline__ Walk(const PagedBatch& p, int TB, const Start* st)
-      : f(st->f0), f1(st->f1), b(st->b), g(st->g), i(st->i), t0(st->t) {
-    s = load_seq(p, b);
+  __device__ __forceinline__ Walk(int TB, const Start* st)
+      : f(st->f0), f1(st->f1), b(st->b), g(st->g), i(st->i), t0(st->t), s(st->s) {
     span(TB);
   }
   __device__ __forceinline__ bool more() const { return f < f1; }
@@ -197,20 +234,28 @@ struct Walk {
   }
 };
 
-// What a CTA leaves in the workspace for the merging kernel: where its share begins.
+// What CTA c leaves in the workspace for the merging kernel: the item that the border at the
+// start of its share is the first to cut (tokens = 0: none).
 struct Mark {
-  int64_t per, f0, b;
-  int32_t g, i, t, any;
+  int64_t row;     // packed row of the item's first token
+  int64_t c0;      // CTA of its first segment
+  int32_t n;       // segments, in CTAs c0 .. c0 + n - 1
+  int32_t late;    // the first segment is its CTA's last one, not its first
+  int32_t tokens;  // of the item
+  int32_t g;       // KV head
 };
-__device__ __forceinline__ void leave_mark(const Start* st, Mark* m) {
-  Mark v;
-  v.per = st->per;
-  v.f0 = st->f0;
-  v.b = st->b;
-  v.g = st->g;
-  v.i = st->i;
-  v.t = st->t;
-  v.any = st->any;
+__device__ __forceinline__ void leave_mark(const Start* st, int TB, int64_t c, Mark* m) {
+  Mark v = {};
+  if (st->any && st->t > 0 && st->t <= st->per) {  // not cut at an earlier border already
+    const int64_t start = st->f0 - st->t, end = start + block_tiles(st->s, TB, st->i);
+    v.row = st->s.q0 + (int64_t)st->i * TB;
+    v.c0 = c - 1;
+    v.late = st->t != st->per;
+    v.n = 2;
+    for (int64_t at = st->f1; at < end; at += st->per) ++v.n;
+    v.tokens = min(TB, st->s.nq - st->i * TB);
+    v.g = st->g;
+  }
   *m = v;
 }
 
@@ -224,12 +269,12 @@ __host__ __device__ inline size_t slot_floats(int rows, int dh) {
 // segments can belong to cut items).
 __device__ __forceinline__ int64_t slot_of(int64_t c, int64_t f, int64_t f0) { return 2 * c + (f == f0 ? 0 : 1); }
 
-// The merging kernel (paged_attn.cu): one item per border that is the first to cut it.
+// The merging kernel (paged_attn.cu): O and lse of the items the marks name.
 struct MergeArgs {
-  PagedBatch p;
   const Mark* marks;
   const float* slots;
-  int rows, TB, G, Hq;
+  int64_t N;
+  int rows, G, Hq;
   float unit_log2;  // row maxima times this are in the log2 domain
   void* O;
   float* lse;

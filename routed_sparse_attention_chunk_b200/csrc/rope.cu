@@ -5,10 +5,9 @@
 //   y = (a c - b s, a s + b c)     transposed: (a c + b s, b c - a s)
 // in fp32, rounded once on the store; the dimensions past rd are copied.
 //
-// Bound by memory (3 flop per 8 bytes): every 16-byte vector of x is read and
-// written once, and a token's table row is read by its heads through L1.  A
-// thread takes one unit: two vectors rd/2 apart (half layout), or one vector
-// holding whole pairs (interleaved, and the copied tail).
+// Bound by memory (3 flop per 8 bytes): every vector of x is read and written
+// once.  A thread takes one unit (two vectors) of up to four heads of a token, so
+// the table's pairs are read once for them and eight loads are in flight.
 #include "common.cuh"
 #include "internal.h"
 #include "rope.cuh"
@@ -16,37 +15,57 @@
 namespace msa {
 namespace {
 
-// Launched as a programmatic dependent: it may start while the previous kernel of the stream
-// drains, and reads nothing that kernel writes before this wait.
-template <typename T>
-__global__ void __launch_bounds__(256) rope_kernel(RopeArgs a, int units, int64_t total) {
+// A programmatic dependent: it may start while the previous kernel of the stream
+// drains, and reads nothing that kernel writes before the wait.
+template <typename T, bool kInter>
+__global__ void __launch_bounds__(256) rope_kernel(RopeArgs a, int units, int groups, int64_t total) {
   pdl_wait();
-  const int64_t step = (int64_t)gridDim.x * blockDim.x;
-  for (int64_t u = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; u < total; u += step) {
-    const int64_t row = u / units;  // token * H + head
-    const int unit = (int)(u - row * units);
-    const int64_t n = row / a.H;
-    const int h = (int)(row - n * a.H);
-    const int pos = __ldg(a.pos + n);
-    if (pos < 0 || pos >= a.max_len) {
-      if (unit == 0 && h == 0) raise_flag(a.err_flag, MSA_FLAG_INDEX_OOB);
-      continue;
+  const int64_t id = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (id >= total) return;
+  const uint32_t per = (uint32_t)(units * groups);
+  const int64_t n = total < 0xffffffffll ? (int64_t)((uint32_t)id / per) : id / per;
+  const uint32_t r = (uint32_t)(id - n * per), hg = r / (uint32_t)units, u = r - hg * (uint32_t)units;
+  const int pos = __ldg(a.pos + n);
+  const RopeUnit<T> unit((int)u, a.rd, kInter);
+  const T* x = reinterpret_cast<const T*>(a.x) + n * a.x_ts;
+  T* y = reinterpret_cast<T*>(a.out) + n * a.out_ts;
+  uint4 p[kRopeHeads], q[kRopeHeads];
+#pragma unroll
+  for (int j = 0; j < kRopeHeads; ++j) {
+    const int h = (int)hg + j * groups;
+    if (h < a.H) {
+      const T* src = x + h * a.x_hs;
+      p[j] = *reinterpret_cast<const uint4*>(src + unit.at0);
+      q[j] = *reinterpret_cast<const uint4*>(src + unit.at1);
     }
-    const T* x = reinterpret_cast<const T*>(a.x) + n * a.x_ts + h * a.x_hs;
-    T* y = reinterpret_cast<T*>(a.out) + n * a.out_ts + h * a.out_hs;
-    rotate_unit<T>(x, y, unit, a.rd, a.interleaved, a.transpose, a.cs + (int64_t)pos * a.rd);
+  }
+  if (pos < 0 || pos >= a.max_len) {
+    if (r == 0) raise_flag(a.err_flag, MSA_FLAG_INDEX_OOB);
+    return;
+  }
+  RopeTurn<T> turn;
+  if (unit.rotated) turn.load(a.cs + (int64_t)pos * a.rd, (int)u, a.transpose ? -1.f : 1.f);
+#pragma unroll
+  for (int j = 0; j < kRopeHeads; ++j) {
+    const int h = (int)hg + j * groups;
+    if (h < a.H) {
+      if (unit.rotated) turn.apply(p[j], q[j], kInter);
+      T* dst = y + h * a.out_hs;
+      *reinterpret_cast<uint4*>(dst + unit.at0) = p[j];
+      *reinterpret_cast<uint4*>(dst + unit.at1) = q[j];
+    }
   }
 }
 
 template <typename T>
 cudaError_t rope_t(const RopeArgs& a, cudaStream_t s) {
-  const int units = rope_units<T>(a.d, a.rd, a.interleaved);
-  const int64_t total = a.N * a.H * units;
+  const int units = RopeUnit<T>::per_head(a.d), groups = (a.H + kRopeHeads - 1) / kRopeHeads;
+  const int64_t total = a.N * units * groups;
   const int64_t blocks = (total + 255) / 256;
-  // grid x holds 2^31 - 1 blocks; the kernel strides over the rest
-  const unsigned grid = (unsigned)(blocks < 0x7fffffff ? blocks : 0x7fffffff);
+  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;  // grid x
   count_launch();
-  return launch_pdl(rope_kernel<T>, dim3(grid), dim3(256), 0, s, a, units, total);
+  return launch_pdl(a.interleaved ? rope_kernel<T, true> : rope_kernel<T, false>, dim3((unsigned)blocks), dim3(256), 0,
+                    s, a, units, groups, total);
 }
 
 }  // namespace

@@ -1,60 +1,66 @@
-// The rotation of one head, in 16-byte units (rope.cu, paged_append.cu).
+// The rotation of heads in units of two 16-byte vectors (rope.cu, paged_append.cu).
 #pragma once
 
 #include "common.cuh"
 
 namespace msa {
 
-// Units of one head of d dimensions of which rd are rotated (rd and d multiples of
-// 2 * Vec<T>::N): half layout: a unit is the vectors at i and i + rd / 2; interleaved: a
-// unit is one vector of whole pairs; past rd one vector, copied.
+// Unit u of a head of d dimensions, rd of them rotated (both multiples of 16): N =
+// Vec<T>::N pairs u N .. u N + N - 1 of the rotation, or 2 N of the dimensions past it.
+// Its two vectors lie rd / 2 apart in the half layout, side by side otherwise.
 template <typename T>
-__host__ __device__ __forceinline__ int rope_units(int d, int rd, bool interleaved) {
-  const int rot = interleaved ? rd / Vec<T>::N : rd / 2 / Vec<T>::N;
-  return rot + (d - rd) / Vec<T>::N;
-}
+struct RopeUnit {
+  static constexpr int N = Vec<T>::N;
+  int at0, at1;
+  bool rotated;
+  __device__ __forceinline__ RopeUnit(int u, int rd, bool interleaved) {
+    rotated = u * 2 * N < rd;
+    const bool half = rotated && !interleaved;
+    at0 = half ? u * N : u * 2 * N;
+    at1 = half ? at0 + rd / 2 : at0 + N;
+  }
+  static __host__ __device__ __forceinline__ int per_head(int d) { return d / (2 * N); }
+};
 
+// (cos, sin) of the unit's N pairs; the transposed rotation turns the other way.
 template <typename T>
-__device__ __forceinline__ void rotate_unit(const T* x, T* y, int unit, int rd, bool interleaved, bool transpose,
-                                            const float* cs) {
-  constexpr int N = Vec<T>::N;
-  const int rot = interleaved ? rd / N : rd / 2 / N;
-  if (unit >= rot) {  // past the rotated part
-    const int at = rd + (unit - rot) * N;
-    if (x != y) *reinterpret_cast<uint4*>(y + at) = *reinterpret_cast<const uint4*>(x + at);
-    return;
-  }
-  const float sg = transpose ? -1.f : 1.f;
-  if (interleaved) {
-    const int at = unit * N;
-    float v[N];
-    unpack(*reinterpret_cast<const uint4*>(x + at), v);
+struct RopeTurn {
+  static constexpr int N = Vec<T>::N;
+  float c[N], s[N];
+  __device__ __forceinline__ void load(const float* cs, int u, float sign) {
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
-      const float2 t = __ldg(reinterpret_cast<const float2*>(cs + at + i));  // pair (at + i) / 2
-      const float a = v[i], b = v[i + 1], sn = sg * t.y;
-      v[i] = a * t.x - b * sn;
-      v[i + 1] = a * sn + b * t.x;
+      const float4 t = __ldg(reinterpret_cast<const float4*>(cs + 2 * (u * N + i)));
+      c[i] = t.x;
+      s[i] = sign * t.y;
+      c[i + 1] = t.z;
+      s[i + 1] = sign * t.w;
     }
-    *reinterpret_cast<uint4*>(y + at) = pack(v);
-  } else {
-    const int at = unit * N, half = rd / 2;
+  }
+  __device__ __forceinline__ void turn(float& a, float& b, int i) const {
+    const float x = a * c[i] - b * s[i];
+    b = a * s[i] + b * c[i];
+    a = x;
+  }
+  __device__ __forceinline__ void apply(uint4& p, uint4& q, bool interleaved) const {
     float v[N], w[N];
-    unpack(*reinterpret_cast<const uint4*>(x + at), v);
-    unpack(*reinterpret_cast<const uint4*>(x + at + half), w);
+    unpack(p, v);
+    unpack(q, w);
+    if (interleaved) {
 #pragma unroll
-    for (int i = 0; i < N; i += 2) {
-      const float4 t = __ldg(reinterpret_cast<const float4*>(cs + 2 * (at + i)));  // pairs at + i, at + i + 1
-      const float a0 = v[i], b0 = w[i], s0 = sg * t.y;
-      const float a1 = v[i + 1], b1 = w[i + 1], s1 = sg * t.w;
-      v[i] = a0 * t.x - b0 * s0;
-      w[i] = a0 * s0 + b0 * t.x;
-      v[i + 1] = a1 * t.z - b1 * s1;
-      w[i + 1] = a1 * s1 + b1 * t.z;
+      for (int i = 0; i < N; i += 2) {
+        turn(v[i], v[i + 1], i / 2);
+        turn(w[i], w[i + 1], N / 2 + i / 2);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) turn(v[i], w[i], i);
     }
-    *reinterpret_cast<uint4*>(y + at) = pack(v);
-    *reinterpret_cast<uint4*>(y + at + half) = pack(w);
+    p = pack(v);
+    q = pack(w);
   }
-}
+};
+
+constexpr int kRopeHeads = 4;  // heads a thread takes, all of their loads in flight at once
 
 }  // namespace msa

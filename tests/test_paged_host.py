@@ -204,7 +204,7 @@ class _Fake:
 
 @pytest.fixture
 def device0(monkeypatch):
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
 
 
 def test_binding_refusals(device0):
