@@ -28,6 +28,7 @@ namespace {
 
 constexpr int kSub = 32;  // keys per step of the fp32 kernel
 constexpr int kF32Threads = 256;
+constexpr int kF32Slack = 2;  // tiles that not merging cut items is worth
 
 template <int DH, int RPT>
 struct F32Smem {
@@ -50,7 +51,7 @@ __global__ void __launch_bounds__(kF32Threads) paged_f32_kernel(PagedAttnArgs a,
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
   const int G = a.Hq / p.Hkv;
   pdl_wait();
-  find_start(p, TB, blockIdx.x, gridDim.x, blockIdx.x == 0, &sm.st);
+  find_start(p, TB, kF32Slack, blockIdx.x, gridDim.x, blockIdx.x == 0, &sm.st, reinterpret_cast<ScanScratch*>(sm.row));
   if (tid == 0) leave_mark(&sm.st, TB, blockIdx.x, marks + blockIdx.x);
   pdl_trigger();
   if (!sm.st.any) return;
@@ -211,65 +212,68 @@ __global__ void __launch_bounds__(kF32Threads) paged_f32_kernel(PagedAttnArgs a,
 // O = sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s over an item's segments, in the
 // order of the CTAs.  Block x merges the item of mark x + 1, if there is one; block y
 // takes kMergeRows of its rows, a thread four values of a row.  A chain of dependent
-// loads (mark, maxima, values) bounds it, so few rows per block: all are in flight.
-constexpr int kMergeRows = 8;
+// loads (mark, maxima, values) bounds it; all blocks are resident at once.
+constexpr int kMergeThreads = 256, kMergeRows = 32;
 template <typename T, int DH, bool kQuads>
-__global__ void __launch_bounds__(kMergeRows * (DH / 4)) merge_kernel(MergeArgs a) {
+__global__ void __launch_bounds__(kMergeThreads) merge_kernel(MergeArgs a) {
+  constexpr int kPairs = kMergeRows * (DH / 4);  // (row, four values) pairs of the block
   pdl_wait();
-  const int64_t c = (int64_t)blockIdx.x + 1;
-  const Mark mk = a.marks[c];
-  // consecutive threads: rows first in the quads layout, values of a row first in the other
-  const int quad = kQuads ? threadIdx.x / kMergeRows : threadIdx.x % (DH / 4);
-  const int r = blockIdx.y * kMergeRows + (kQuads ? threadIdx.x % kMergeRows : threadIdx.x / (DH / 4));
-  const int tl = r / a.G, hh = r - tl * a.G;
-  if (tl >= mk.tokens) return;
+  const Mark mk = a.marks[blockIdx.x + 1];
+  const int last = mk.tokens * a.G;  // rows of the item
   const size_t sf = slot_floats(a.rows, DH);
   const float* first = a.slots + (2 * mk.c0 + mk.late) * sf;
   const float* rest = a.slots + 2 * mk.c0 * sf;  // segment x > 0 is in slot 2 (c0 + x)
-  const int ml_at = a.rows * DH + 2 * r, v_at = kQuads ? (quad * a.rows + r) * 4 : r * DH + quad * 4;
-  float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int x0 = 0; x0 < mk.n; x0 += 4) {
-    float2 ml[4];
-    float4 v[4];
-    float top = m;
+#pragma unroll 2
+  for (int e = threadIdx.x; e < kPairs; e += kMergeThreads) {
+    // consecutive threads: rows first in the quads layout, values of a row first in the other
+    const int quad = kQuads ? e / kMergeRows : e % (DH / 4);
+    const int r = blockIdx.y * kMergeRows + (kQuads ? e % kMergeRows : e / (DH / 4));
+    if (r >= last) continue;
+    const int ml_at = a.rows * DH + 2 * r, v_at = kQuads ? (quad * a.rows + r) * 4 : r * DH + quad * 4;
+    float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int x0 = 0; x0 < mk.n; x0 += 4) {
+      float2 ml[4];
+      float4 v[4];
+      float top = m;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (x0 + j >= mk.n) continue;
-      const float* src = x0 + j == 0 ? first : rest + 2 * (size_t)(x0 + j) * sf;
-      ml[j] = *reinterpret_cast<const float2*>(src + ml_at);
-      v[j] = *reinterpret_cast<const float4*>(src + v_at);
+      for (int j = 0; j < 4; ++j) {
+        if (x0 + j >= mk.n) continue;
+        const float* src = x0 + j == 0 ? first : rest + 2 * (size_t)(x0 + j) * sf;
+        ml[j] = *reinterpret_cast<const float2*>(src + ml_at);
+        v[j] = *reinterpret_cast<const float4*>(src + v_at);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (x0 + j < mk.n) top = fmaxf(top, ml[j].x);
+      const float corr = l == 0.f ? 0.f : exp2f((m - top) * a.unit_log2);
+      l *= corr;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] *= corr;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (x0 + j >= mk.n) continue;
+        const float w = ml[j].y == 0.f ? 0.f : exp2f((ml[j].x - top) * a.unit_log2);  // sum 0: no key was visible
+        l += w * ml[j].y;
+        acc[0] += w * v[j].x;
+        acc[1] += w * v[j].y;
+        acc[2] += w * v[j].z;
+        acc[3] += w * v[j].w;
+      }
+      m = top;
     }
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (x0 + j < mk.n) top = fmaxf(top, ml[j].x);
-    const float corr = l == 0.f ? 0.f : exp2f((m - top) * a.unit_log2);
-    l *= corr;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] *= corr;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (x0 + j >= mk.n) continue;
-      const float w = ml[j].y == 0.f ? 0.f : exp2f((ml[j].x - top) * a.unit_log2);  // sum 0: no key was visible
-      l += w * ml[j].y;
-      acc[0] += w * v[j].x;
-      acc[1] += w * v[j].y;
-      acc[2] += w * v[j].z;
-      acc[3] += w * v[j].w;
-    }
-    m = top;
+    const bool seen = l != 0.f;
+    const float inv = seen ? 1.f / l : 0.f;
+    const int tl = r / a.G, h = mk.g * a.G + (r - tl * a.G);
+    const int64_t row = mk.row + tl;
+    T* dst = reinterpret_cast<T*>(a.O) + (row * a.Hq + h) * DH + quad * 4;
+    if constexpr (sizeof(T) == 4)
+      *reinterpret_cast<float4*>(dst) = make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
+    else
+      *reinterpret_cast<uint2*>(dst) =
+          make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+    if (a.lse && quad == 0)
+      a.lse[(int64_t)h * a.N + row] = seen ? (m * a.unit_log2 + log2f(l)) * 0.69314718055994531f : -INFINITY;
   }
-  const bool seen = l != 0.f;
-  const float inv = seen ? 1.f / l : 0.f;
-  const int64_t row = mk.row + tl;
-  const int h = mk.g * a.G + hh;
-  T* dst = reinterpret_cast<T*>(a.O) + (row * a.Hq + h) * DH + quad * 4;
-  if constexpr (sizeof(T) == 4)
-    *reinterpret_cast<float4*>(dst) = make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
-  else
-    *reinterpret_cast<uint2*>(dst) =
-        make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
-  if (a.lse && quad == 0)
-    a.lse[(int64_t)h * a.N + row] = seen ? (m * a.unit_log2 + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
 template <int DH, int RPT>
@@ -296,12 +300,11 @@ bool few_rows(int Hq, int Hkv, int max_q) { return (int64_t)(Hq / Hkv) * max_q <
 cudaError_t launch_merge(msa_dtype dt, int d, bool quads, const MergeArgs& a, int grid, cudaStream_t s) {
   if (grid < 2) return cudaSuccess;
   const dim3 g((unsigned)(grid - 1), (unsigned)((a.rows + kMergeRows - 1) / kMergeRows));
-  const dim3 t((unsigned)(kMergeRows * (d / 4)));
   auto k = dt == MSA_F32 ? (d == 64 ? merge_kernel<float, 64, false> : merge_kernel<float, 128, false>)
            : !quads      ? merge_kernel<__nv_bfloat16, 128, false>
                          : (d == 64 ? merge_kernel<__nv_bfloat16, 64, true> : merge_kernel<__nv_bfloat16, 128, true>);
   count_launch();
-  return launch_pdl(k, g, t, 0, s, a);
+  return launch_pdl(k, g, dim3(kMergeThreads), 0, s, a);
 }
 
 }  // namespace paged

@@ -41,6 +41,7 @@ constexpr int kStages = 3;
 constexpr int kThreads = 192;
 constexpr uint32_t kWaitPolls = 1u << 24;
 constexpr uint32_t kSpinLimit = 1u << 28;  // non-blocking polls of the MMA issuer without progress
+constexpr int kSlack = 4;  // tiles that not merging cut items is worth
 constexpr float kRescaleLog2 = 8.0f;
 
 struct DecParams {
@@ -147,7 +148,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmKm, const __grid_const
   }
   // a programmatic dependent: nothing an earlier kernel writes is read before this wait
   pdl_wait();
-  find_start(p, TB, blockIdx.x, gridDim.x, blockIdx.x == 0, start);
+  find_start(p, TB, kSlack, blockIdx.x, gridDim.x, blockIdx.x == 0, start, reinterpret_cast<ScanScratch*>(red_s));
   if (tid == 0) leave_mark(start, TB, blockIdx.x, a.marks + blockIdx.x);
   pdl_trigger();
   if (!start->any) return;

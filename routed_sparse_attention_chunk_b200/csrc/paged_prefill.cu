@@ -5,29 +5,35 @@
 // head, so one K/V tile serves every head of the group.  Per 128-key tile:
 //   S = Q K^T by tcgen05.mma into one of two TMEM buffers (Q copied into tensor
 //   memory once per item, K from its TMA tile);
-//   P = 2^(scale log2(e) S - m), one row per thread, rounded to bf16 over its own
-//   S buffer (2^-9 per weight, averaged over the keys; the row sum is taken from
-//   the fp32 values);
+//   P = 2^(scale log2(e) S - m), one row per thread, rounded to bf16 (2^-9 per
+//   weight on average less, over many keys; the row sum is taken from the fp32
+//   values), into tensor memory;
 //   O += P V (P from tensor memory, V MN-major from its tile).
-// S and PV have their own issuing threads; K and V of a tile share one of three
-// stages and one barrier.  The running maximum moves (and O is rescaled in TMEM)
-// only when it grows by more than 2^8; the sum uses the same maximum, so the
-// result is exact.  A row that has seen no key yet keeps the maximum -inf and
-// weights of 0.
+// Two softmax warpgroups take the tiles in turn, so that one's exponentials run
+// beside the other's loads, maxima and hand-offs (a single one was latency-bound at
+// 2,700 cycles a tile against 1,030 of tensor-core work).  Each keeps a reference
+// maximum of its own per row, a whole number in the log2 domain that moves only
+// when a score passes it by 2^8; a tile's P is brought to O's reference when it is
+// stored, which happens in the tiles' order, and O (in TMEM) is rescaled only when
+// that reference has to grow.  All these factors are powers of two, and the sums of
+// the two are added under O's reference at the item's end, so the result is exact.
+// A row that has seen no key yet keeps the reference -inf and weights of 0.
 // A tile's K and V arrive as one box per page, straight from the block table's
-// pages, or per run of bank rows of the segment plan.  Rows past the sequence's
-// end are masked, and their V rows zeroed in shared memory before the product
-// (0 x NaN is NaN, and a page's tail holds anything).
+// pages, or per run of bank rows of the segment plan, K and V from a warp each
+// (small boxes: the issue rate of one warp was 3,600 cycles a tile for pages of
+// 16), in rings of three.  Rows past the sequence's end are masked, and their V
+// rows zeroed in shared memory before the product (0 x NaN is NaN, and a page's
+// tail holds anything).
 // Persistent: one CTA per SM walks its equal share of all (item, tile) pairs
 // (paged_sched.cuh).  The pipeline runs through item borders: the next item's Q
-// rows are copied to shared memory during the current item and into the other of
-// two TMEM buffers behind its last tile, so the next S runs while the current
-// item's output is written.
-// Warp roles (224 threads): warp 0 TMA producer, warp 1 TMEM owner + S issuer,
-// warps 2..5 softmax / output (one row per thread), warp 6 PV issuer.  Every
-// wait is bounded and ends the CTA with MSA_FLAG_TIMEOUT on expiry.
-#include <type_traits>
-
+// rows wait in shared memory, and move to tensor memory as soon as the current
+// item's last S is done; the warpgroup without the last tile goes on to the next
+// item while the other writes the output.
+// Warp roles (384 threads): warp 0 K producer, warp 1 TMEM owner + S issuer, warp 2
+// PV issuer, warp 3 V producer, warps 4..7 and 8..11 softmax / output
+// (one row per thread), which take registers from the first four.  Every wait is
+// bounded; after the first that runs out the softmax warps go on without data, the
+// others stop, and MSA_FLAG_TIMEOUT is raised.
 #include "common.cuh"
 #include "internal.h"
 #include "paged_sched.cuh"
@@ -41,8 +47,10 @@ using namespace sm100;
 using namespace paged;
 
 constexpr int kRows = 128;     // MMA M: query rows per block
-constexpr int kThreads = 224;  // producer, S issuer, four softmax warps, PV issuer
+constexpr int kThreads = 384;  // K producer, S issuer, PV issuer, V producer, 2 x 4 softmax warps
+constexpr int kSoftRegs = 216, kOtherRegs = 72;  // 256 x 216 + 128 x 72 = 384 x 168, the launch's registers
 constexpr uint32_t kWaitPolls = 1u << 24;
+constexpr int kSlack = 8;  // tiles that not merging cut items is worth
 constexpr float kRescaleLog2 = 8.0f;  // move the running max only when it grows by more than this
 
 struct PreParams {
@@ -53,6 +61,7 @@ struct PreParams {
   const uint8_t* seg_cnt;
   int Hq, G, TB;
   int box_rows;  // rows of one box: min(page, 128)
+  int page_shift;
   __nv_bfloat16* O;
   float* lse;
   Mark* marks;
@@ -62,14 +71,15 @@ struct PreParams {
 
 template <int DH>
 struct Layout {
-  static constexpr int kKV = 3;                // K + V stages
+  static constexpr int kKV = 3;                // stages of the K ring and of the V ring
   static constexpr int kBoxes = DH / 64;
   static constexpr int kQ = kRows * DH * 2;    // the next item's query rows on their way to tensor memory
   static constexpr int kK = kKeys * DH * 2;    // one K (or V) tile
-  static constexpr int kBar = 8 * 24;
-  static constexpr int kSmem = 1024 + kQ + 2 * kKV * kK + kBar + (int)sizeof(Start);
-  static constexpr uint32_t kTmemCols = 512;   // S0, S1 (128 each), O (DH), Q0, Q1 (DH / 2 each)
-  static_assert(2 * kKeys + 2 * DH <= (int)kTmemCols, "tensor memory columns");
+  static constexpr int kBars = 30;
+  static constexpr int kRowState = kRows * 4 + kRows * 8;  // O's references; one warpgroup's (reference, sum)
+  static constexpr int kSmem = 1024 + kQ + 2 * kKV * kK + 8 * kBars + kRowState + (int)sizeof(Start);
+  static constexpr uint32_t kTmemCols = 512;   // S0, S1 (128 each), O (DH), P (64), Q (DH / 2)
+  static_assert(2 * kKeys + DH + kKeys / 2 + DH / 2 <= (int)kTmemCols, "tensor memory columns");
   static_assert(kSmem <= 232448, "shared memory of one CTA");
 };
 
@@ -79,9 +89,10 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-// 16 bytes from global to shared memory without passing registers; completes at cp_async_wait.
-__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+// 16 bytes from global to shared memory without passing registers (zeros if !have).
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool have) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(have ? 16 : 0)
+               : "memory");
 }
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
@@ -111,38 +122,6 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
   return d;
 }
 
-// 2^x for a pair of arguments on the FMA and integer pipes, leaving the
-// transcendental unit (whose ex2 throughput bounds the softmax) to the other
-// keys: x = j + f with j = round(x) (read from the mantissa of x + 1.5 * 2^23)
-// and f in [-1/2, 1/2]; 2^f by a cubic whose coefficients are a weighted
-// least-squares fit of 2^f on [-1/2, 1/2] at Chebyshev nodes refined by Lawson
-// iterations toward equal relative error (max relative error 7.5e-5, far below
-// the bf16 rounding of P); 2^j is added to the exponent field.  Arguments below
-// -126 are clamped there (weights below 2^-126 instead of 0; masked keys give
-// 2^-126 * 2^f, which vanishes in the bf16 P and in the row sum's fp32).
-__device__ __forceinline__ void exp2_poly2(float x0, float x1, float& e0, float& e1) {
-  constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
-  const uint64_t x = f2_pack(fmaxf(x0, -126.0f), fmaxf(x1, -126.0f));
-  const uint64_t t = f2_add(x, f2_pack(kMagic, kMagic));         // round(x) in the low mantissa bits
-  const uint64_t jf = f2_add(t, f2_pack(-kMagic, -kMagic));      // round(x) as a float
-  const uint64_t f = f2_fma(jf, f2_pack(-1.0f, -1.0f), x);        // x - round(x)
-  uint64_t q = f2_fma(f, f2_pack(0.0551716648f, 0.0551716648f), f2_pack(0.2426111251f, 0.2426111251f));
-  q = f2_fma(q, f, f2_pack(0.6932609677f, 0.6932609677f));
-  q = f2_fma(q, f, f2_pack(0.9999280572f, 0.9999280572f));
-  float q0, q1, t0, t1;
-  f2_unpack(q, q0, q1);
-  f2_unpack(t, t0, t1);
-  // the low bits of t hold round(x); shifted by 23 they add it to the exponent
-  e0 = __uint_as_float(__float_as_uint(q0) + (__float_as_uint(t0) << 23));
-  e1 = __uint_as_float(__float_as_uint(q1) + (__float_as_uint(t1) << 23));
-}
-
-// Of each 16 key pairs of a 32-key store, this many take exp2_poly2 (spread
-// evenly); the rest take the transcendental unit's ex2.
-constexpr int kPolyPairs = 6;
-__host__ __device__ constexpr bool poly_pair(int i) { return (i * kPolyPairs) / 16 != ((i + 1) * kPolyPairs) / 16; }
-
-
 template <int DH>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_prefill_kernel(const __grid_constant__ CUtensorMap tmKm, const __grid_constant__ CUtensorMap tmVm,
@@ -155,32 +134,45 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmKm, const __grid_cons
   uint8_t* Vs = Ks + kKV * L::kK;    // [kKV] V tiles
   uint8_t* Qs = Vs + kKV * L::kK;
   uint64_t* bars = reinterpret_cast<uint64_t*>(Qs + L::kQ);
-  uint64_t* kv_full = bars;                // [kKV] K and V of a tile landed
-  uint64_t* kv_empty = kv_full + kKV;      // [kKV] its PV is done
-  uint64_t* s_full = kv_empty + kKV;       // [2] S done -> softmax
-  uint64_t* p_full = s_full + 2;           // [2] P written over S -> PV
-  uint64_t* p_free = p_full + 2;           // [2] PV done (O up to date, S buffer free)
+  uint64_t* k_full = bars;                 // [kKV] K of a tile landed
+  uint64_t* k_empty = k_full + kKV;        // [kKV] its S is done
+  uint64_t* v_full = k_empty + kKV;        // [kKV]
+  uint64_t* v_empty = v_full + kKV;        // [kKV] its PV is done
+  uint64_t* s_full = v_empty + kKV;        // [2] S done -> softmax
+  uint64_t* s_free = s_full + 2;           // [2] S read into registers
+  uint64_t* p_full = s_free + 2;           // P in tensor memory -> PV
+  uint64_t* p_free = p_full + 1;           // [2] PV of an even / odd tile done (O up to date, P free)
   uint64_t* q_tmem = p_free + 2;           // an item's Q is in tensor memory
-  uint64_t* drain_s = q_tmem + 1;
+  uint64_t* o_read = q_tmem + 1;           // an item's O and sums have been read
+  uint64_t* l_ready = o_read + 1;          // [4 warps] the sums of the warpgroup without the last tile
+  uint64_t* drain_s = l_ready + 4;
   uint64_t* drain_pv = drain_s + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_pv + 1);
+  static_assert(4 * kKV + 4 + 3 + 8 <= L::kBars - 1, "barriers");
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + L::kBars - 1);
   volatile int* abort_s = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  Start* start = reinterpret_cast<Start*>(bars + 24);
+  float* m_s = reinterpret_cast<float*>(bars + L::kBars);     // [kRows] O's references, log2 domain
+  float2* ml_s = reinterpret_cast<float2*>(m_s + kRows);      // [kRows] (reference, sum)
+  Start* start = reinterpret_cast<Start*>(ml_s + kRows);
 
   const PagedBatch& p = a.p;
   const int TB = a.TB;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kKV; ++i) {
-      mbar_init(&kv_full[i], 1);
-      mbar_init(&kv_empty[i], 1);
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 128);
+      mbar_init(&s_free[i], 128);
       mbar_init(&p_free[i], 1);
     }
+    mbar_init(p_full, 128);
     mbar_init(q_tmem, 128);
+    mbar_init(o_read, 128);
+    for (int i = 0; i < 4; ++i) mbar_init(&l_ready[i], 32);
     mbar_init(drain_s, 1);
     mbar_init(drain_pv, 1);
     *abort_s = 0;
@@ -188,7 +180,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmKm, const __grid_cons
   }
   // a programmatic dependent: nothing an earlier kernel writes is read before this wait
   pdl_wait();
-  find_start(p, TB, blockIdx.x, gridDim.x, blockIdx.x == 0, start);
+  find_start(p, TB, kSlack, blockIdx.x, gridDim.x, blockIdx.x == 0, start, reinterpret_cast<ScanScratch*>(m_s));
   if (threadIdx.x == 0) leave_mark(start, TB, blockIdx.x, a.marks + blockIdx.x);
   pdl_trigger();
   if (!start->any) return;
@@ -200,155 +192,174 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmKm, const __grid_cons
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  // TMEM columns: S0, S1 (128 each), O (DH), Q0, Q1 as the S MMAs' A operand (DH / 2: bf16 pairs)
-  const uint32_t tS0 = tmem, tO = tmem + 2 * kKeys, tQ0 = tmem + 2 * kKeys + DH;
+  // TMEM columns: S0, S1 (128 each), O (DH), P (64: bf16 pairs), Q as the S MMAs' A operand (DH / 2)
+  const uint32_t tS0 = tmem, tO = tmem + 2 * kKeys, tP = tO + DH, tQ = tP + kKeys / 2;
   auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_or_stop(bar, parity, kWaitPolls, abort_s); };
 
-  if (warp == 0) {
-    // ---------------------------------------------------------------- producer
-    // Lane 0 waits and arms the barriers.  A tile is up to 16 boxes per 64-column
-    // half of K and of V, one lane each: the plan's segments of kSegRows bank rows,
-    // or the pages (parts of pages) that hold cached tokens.  Each lands on a 1 KB
-    // swizzle atom, so the tile's layout is that of one 128-row box.
-    uint32_t it = 0;
-    bool stop = false;
-    for (Walk w(TB, start); w.more() && !stop; w.next(p, TB)) {
-      for (int t = w.t0; t < w.t0 + w.n; ++t, ++it) {
-        const uint32_t st = it % kKV, round = it / kKV;
-        const bool mem = t < w.s.nm;
-        const int key0 = mem ? 0 : (t - w.s.nm) * kKeys;
-        const int rows = mem ? kSegRows : a.box_rows;
+  if (warp < 4) {
+    setmaxnreg_dec<kOtherRegs>();
+    if (warp == 0 || warp == 3) {
+      // -------------------------------------------------------------- K and V producers
+      // Lane 0 waits and arms the barriers.  A tile is up to 16 boxes per 64-column
+      // half, one lane each: the plan's segments of kSegRows bank rows, or the pages
+      // (parts of pages) that hold cached tokens.  Each lands on a 1 KB swizzle atom,
+      // so the tile's layout is that of one 128-row box.  A lane's place in the block
+      // table is looked up one tile ahead.
+      const bool isK = warp == 0;
+      uint8_t* ring = isK ? Ks : Vs;
+      uint64_t* full = isK ? k_full : v_full;
+      uint64_t* empty = isK ? k_empty : v_empty;
+      const CUtensorMap* mapm = isK ? &tmKm : &tmVm;
+      const CUtensorMap* mapl = isK ? &tmKl : &tmVl;
+      struct Box {
         bool mine;
-        int at = 0, in_page = 0;  // bank row, or page and row inside it
-        if (mem) {
-          mine = lane < kTileSegs;
-          if (mine) at = __ldg(a.seg_row + w.b * p.Smax + t * kTileSegs + lane);
+        int at, in_page;  // bank row, or page and row inside it
+      };
+      auto locate = [&](const Walk& w, int t) {
+        Box x{false, 0, 0};
+        if (t < w.s.nm) {
+          x.mine = lane < kTileSegs;
+          if (x.mine) x.at = __ldg(a.seg_row + w.b * p.Smax + t * kTileSegs + lane);
         } else {
-          const int k = key0 + lane * rows;
-          mine = lane * rows < kKeys && k < w.s.len;
-          if (mine) {
-            const int pi = k / p.page;
-            in_page = k - pi * p.page;
-            at = __ldg(p.table + w.b * p.max_pages + pi);
-            if (at < 0 || at >= p.num_pages) {  // read as zeros (a page past the last)
-              raise_flag(p.err_flag, MSA_FLAG_INDEX_OOB);
-              at = (int)p.num_pages;
-            }
+          const int k = (t - w.s.nm) * kKeys + lane * a.box_rows;
+          x.mine = lane * a.box_rows < kKeys && k < w.s.len;
+          if (x.mine) {
+            const int pi = k >> a.page_shift;
+            x.in_page = k - (pi << a.page_shift);
+            x.at = __ldg(p.table + w.b * p.max_pages + pi);
           }
         }
-        const int boxes = __popc(__ballot_sync(0xffffffffu, mine));
-        int ok = 1;
-        if (lane == 0) {
-          ok = wait(&kv_empty[st], (round & 1) ^ 1);
-          if (ok) mbar_arrive_expect_tx(&kv_full[st], (uint32_t)(boxes * rows * DH * 2 * 2));
-        }
-        if (!__shfl_sync(0xffffffffu, ok, 0)) {
-          stop = true;
-          break;
-        }
-        if (mine) {
-          uint8_t* dk = Ks + st * L::kK + lane * (rows * 128);
-          uint8_t* dv = Vs + st * L::kK + lane * (rows * 128);
+        return x;
+      };
+      uint32_t it = 0;
+      bool stop = false;
+      for (Walk w(TB, start); w.more() && !stop; w.next(p, TB)) {
+        Box x = locate(w, w.t0);
+        for (int t = w.t0; t < w.t0 + w.n; ++t, ++it) {
+          const uint32_t st = it % kKV;
+          const bool mem = t < w.s.nm;
+          const int rows = mem ? kSegRows : a.box_rows;
+          if (!mem && x.mine && (x.at < 0 || x.at >= p.num_pages)) {  // read as zeros (a page past the last)
+            raise_flag(p.err_flag, MSA_FLAG_INDEX_OOB);
+            x.at = (int)p.num_pages;
+          }
+          Box nx{false, 0, 0};
+          if (t + 1 < w.t0 + w.n) nx = locate(w, t + 1);
+          const int boxes = __popc(__ballot_sync(0xffffffffu, x.mine));
+          int ok = 1;
+          if (lane == 0) {
+            ok = wait(&empty[st], ((it / kKV) & 1) ^ 1);
+            if (ok) mbar_arrive_expect_tx(&full[st], (uint32_t)(boxes * rows * DH * 2));
+          }
+          if (!__shfl_sync(0xffffffffu, ok, 0)) {
+            stop = true;
+            break;
+          }
+          if (x.mine) {
+            uint8_t* dst = ring + st * L::kK + lane * (rows * 128);
 #pragma unroll
-          for (int dc = 0; dc < L::kBoxes; ++dc) {
-            if (mem) {
-              tma_load_2d(dk + dc * (kKeys * 128), &tmKm, w.g * DH + dc * 64, at, &kv_full[st]);
-              tma_load_2d(dv + dc * (kKeys * 128), &tmVm, w.g * DH + dc * 64, at, &kv_full[st]);
-            } else {
-              tma_load_4d(dk + dc * (kKeys * 128), &tmKl, dc * 64, w.g, in_page, at, &kv_full[st]);
-              tma_load_4d(dv + dc * (kKeys * 128), &tmVl, dc * 64, w.g, in_page, at, &kv_full[st]);
+            for (int dc = 0; dc < L::kBoxes; ++dc) {
+              if (mem) tma_load_2d(dst + dc * (kKeys * 128), mapm, w.g * DH + dc * 64, x.at, &full[st]);
+              else tma_load_4d(dst + dc * (kKeys * 128), mapl, dc * 64, w.g, x.in_page, x.at, &full[st]);
             }
           }
+          x = nx;
         }
       }
-    }
-    if (lane == 0) {
       // the copies in flight land before the CTA leaves its shared memory
-      for (uint32_t st = 0; st < (uint32_t)kKV && st < it; ++st)
-        if (!mbar_wait(&kv_full[st], ((it - 1 - st) / kKV) & 1, kWaitPolls)) *abort_s = 1;
-    }
-  } else if (warp == 1) {
-    // ---------------------------------------------------------------- S issuer
-    if (lane == 0) {
-      constexpr uint32_t idS = idesc_bf16_f32(kRows, kKeys);
-      // descriptors of the operand bases; a k-step adds its byte offset / 16 to
-      // the 14-bit start-address field (shared addresses stay below 256 KB, so
-      // the field never carries)
-      const uint64_t dk0 = desc_k_sw128(smem_u32(Ks));
-      uint32_t g = 0, nseg = 0;
-      bool ok = true;
-      for (Walk w(TB, start); ok && w.more(); w.next(p, TB), ++nseg) {
-        const uint32_t tQ = tQ0 + (nseg & 1) * (DH / 2);
-        ok = wait(q_tmem, nseg & 1);
-        for (int j = 0; ok && j < w.n; ++j, ++g) {
-          // S goes into buffer g & 1 once the PV of tile g - 2 has read P from it
-          if (g >= 2 && !(ok = wait(&p_free[g & 1], ((g - 2) >> 1) & 1))) break;
-          const uint32_t ks = g % kKV;
-          if (!(ok = wait(&kv_full[ks], (g / kKV) & 1))) break;
-          tc_fence_after();
-          const uint64_t dk = dk0 + (uint64_t)((ks * L::kK) >> 4);
+      if (lane == 0) {
+        for (uint32_t st = 0; st < (uint32_t)kKV && st < it; ++st)
+          if (!mbar_wait(&full[st], ((it - 1 - st) / kKV) & 1, kWaitPolls)) *abort_s = 1;
+      }
+    } else if (warp == 1) {
+      // -------------------------------------------------------------- S issuer
+      if (lane == 0) {
+        constexpr uint32_t idS = idesc_bf16_f32(kRows, kKeys);
+        // descriptors of the operand bases; a k-step adds its byte offset / 16 to
+        // the 14-bit start-address field (shared addresses stay below 256 KB, so
+        // the field never carries)
+        const uint64_t dk0 = desc_k_sw128(smem_u32(Ks));
+        uint32_t g = 0, nseg = 0;
+        bool ok = true;
+        for (Walk w(TB, start); ok && w.more(); w.next(p, TB), ++nseg) {
+          ok = wait(q_tmem, nseg & 1);
+          for (int j = 0; ok && j < w.n; ++j, ++g) {
+            const uint32_t ks = g % kKV;
+            // S goes into buffer g & 1 once the softmax has read tile g - 2 from it
+            if (!(ok = wait(&s_free[g & 1], ((g >> 1) & 1) ^ 1)) || !(ok = wait(&k_full[ks], (g / kKV) & 1))) break;
+            tc_fence_after();
+            const uint64_t dk = dk0 + (uint64_t)((ks * L::kK) >> 4);
 #pragma unroll
-          for (int k = 0; k < DH / 16; ++k) {
-            // A = Q from TMEM (16 elements of bf16 per step are 8 columns), B = K from its tile
-            const int box = k >> 2, kk = k & 3;
-            mma_bf16_ts(tS0 + (g & 1) * kKeys, tQ + k * 8, dk + (uint64_t)((box * kKeys * 128 + kk * 32) >> 4), idS,
-                        k > 0 ? 1u : 0u);
+            for (int k = 0; k < DH / 16; ++k) {
+              // A = Q from TMEM (16 elements of bf16 per step are 8 columns), B = K from its tile
+              const int box = k >> 2, kk = k & 3;
+              mma_bf16_ts(tS0 + (g & 1) * kKeys, tQ + k * 8, dk + (uint64_t)((box * kKeys * 128 + kk * 32) >> 4), idS,
+                          k > 0 ? 1u : 0u);
+            }
+            mma_commit(&s_full[g & 1]);
+            mma_commit(&k_empty[ks]);
           }
-          mma_commit(&s_full[g & 1]);
         }
+        mma_commit(drain_s);
+        if (!mbar_wait(drain_s, 0, kWaitPolls)) *abort_s = 1;
       }
-      mma_commit(drain_s);
-      if (!mbar_wait(drain_s, 0, kWaitPolls)) *abort_s = 1;
-    }
-  } else if (warp == 6) {
-    // ---------------------------------------------------------------- PV issuer
-    if (lane == 0) {
-      constexpr uint32_t idO = idesc_bf16_f32(kRows, DH, /*b_mn_major=*/true);
-      const uint64_t dv0 = desc_mn_sw128(smem_u32(Vs), kKeys * 128);
-      uint32_t g = 0;
-      bool ok = true;
-      for (Walk w(TB, start); ok && w.more(); w.next(p, TB)) {
-        for (int j = 0; ok && j < w.n; ++j, ++g) {
-          const uint32_t st = g & 1, vs = g % kKV;
-          // P written over S; V landed with K
-          if (!(ok = wait(&p_full[st], (g >> 1) & 1)) || !(ok = wait(&kv_full[vs], (g / kKV) & 1))) break;
-          tc_fence_after();
-          const uint64_t dv = dv0 + (uint64_t)((vs * L::kK) >> 4);
-          // A = P from TMEM: 16 keys of bf16 per step are 8 columns
+    } else {
+      // -------------------------------------------------------------- PV issuer
+      if (lane == 0) {
+        constexpr uint32_t idO = idesc_bf16_f32(kRows, DH, /*b_mn_major=*/true);
+        const uint64_t dv0 = desc_mn_sw128(smem_u32(Vs), kKeys * 128);
+        uint32_t g = 0, nseg = 0;
+        bool ok = true;
+        for (Walk w(TB, start); ok && w.more(); w.next(p, TB), ++nseg) {
+          // the first PV of an item overwrites O once the last one has been read
+          if (nseg > 0) ok = wait(o_read, (nseg - 1) & 1);
+          for (int j = 0; ok && j < w.n; ++j, ++g) {
+            const uint32_t vs = g % kKV;
+            if (!(ok = wait(&v_full[vs], (g / kKV) & 1)) || !(ok = wait(p_full, g & 1))) break;
+            tc_fence_after();
+            const uint64_t dv = dv0 + (uint64_t)((vs * L::kK) >> 4);
+            // A = P from TMEM: 16 keys of bf16 per step are 8 columns
 #pragma unroll
-          for (int k = 0; k < kKeys / 16; ++k)
-            mma_bf16_ts(tO, tS0 + st * kKeys + k * 8, dv + (uint64_t)((k * 16 * 128) >> 4), idO,
-                        (j > 0 || k > 0) ? 1u : 0u);
-          mma_commit(&p_free[st]);
-          mma_commit(&kv_empty[vs]);
+            for (int k = 0; k < kKeys / 16; ++k)
+              mma_bf16_ts(tO, tP + k * 8, dv + (uint64_t)((k * 16 * 128) >> 4), idO, (j > 0 || k > 0) ? 1u : 0u);
+            mma_commit(&p_free[g & 1]);
+            mma_commit(&v_empty[vs]);
+          }
         }
+        mma_commit(drain_pv);
+        if (!mbar_wait(drain_pv, 0, kWaitPolls)) *abort_s = 1;
       }
-      mma_commit(drain_pv);
-      if (!mbar_wait(drain_pv, 0, kWaitPolls)) *abort_s = 1;
     }
   } else {
     // ---------------------------------------------------------------- softmax
+    setmaxnreg_inc<kSoftRegs>();
+    const int wg = (warp >> 2) - 1;                   // takes the tiles with g & 1 == wg
     const int q = warp & 3;
     const int r = q * 32 + lane;                      // this thread's row (TMEM lane)
     const int tl = r / a.G, hh = r - tl * a.G;        // token of the block and head of the group
     const uint32_t lane_off = (uint32_t)(q * 32) << 16;
     const float sl2 = a.scale_log2;
-    uint8_t* qrow = Qs + r * (DH * 2);
-    // this row of an item's queries into shared memory (zeros for a row that does not exist); the
-    // 16-byte pieces swizzled by the row so that a warp's reads spread over the banks
-    auto fetch_q = [&](const Walk& w) {
-      const int t = w.i * TB + tl;
-      const bool have = tl < TB && t < w.s.nq;
-      const __nv_bfloat16* src = a.Q + (w.s.q0 + t) * a.q_ts + (w.g * a.G + hh) * DH;
-#pragma unroll
-      for (int c = 0; c < DH / 8; ++c) {
-        uint8_t* dst = qrow + ((c ^ (r & 7)) << 4);
-        if (have) cp_async16(dst, src + c * 8);
-        else *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
-      }
+    // A wait that runs out stops the waiting, not the loops: a warp goes on (without data) to the
+    // end of its share, so that no tcgen05 operation is split among its lanes.
+    auto hold = [&](uint64_t* bar, uint32_t parity) {
+      if (!mbar_test(bar, parity) && !*abort_s) mbar_wait_or_stop(bar, parity, kWaitPolls, abort_s);
+      __syncwarp();
     };
-    // ... and from there into a Q buffer of tensor memory, the S MMAs' A operand
-    auto place_q = [&](uint32_t tQ) {
+    // This row of an item's queries (nullptr: it does not exist) goes to shared memory during the
+    // item before and from there to tensor memory, as the S MMAs' A operand; both by the owner of
+    // that item's last tile.  The 16-byte pieces are swizzled by the row so that a warp's accesses
+    // spread over the banks.
+    uint8_t* qrow = Qs + r * (DH * 2);
+    auto row_of = [&](const Walk& w) -> const __nv_bfloat16* {
+      const int t = w.i * TB + tl;
+      return tl < TB && t < w.s.nq ? a.Q + (w.s.q0 + t) * a.q_ts + (w.g * a.G + hh) * DH : nullptr;
+    };
+    auto fetch_q = [&](const __nv_bfloat16* row) {
+#pragma unroll
+      for (int c = 0; c < DH / 8; ++c)
+        cp_async16(qrow + ((c ^ (r & 7)) << 4), (row ? row : a.Q) + (row ? c * 8 : 0), row != nullptr);
+    };
+    auto place_q = [&]() {
       cp_async_wait();
       __syncwarp();
 #pragma unroll
@@ -368,68 +379,66 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmKm, const __grid_cons
       tc_fence_before();
       mbar_arrive(q_tmem);
     };
-    Walk w(TB, start);
-    fetch_q(w);
-    place_q(tQ0);
-    uint32_t g = 0, nseg = 0;
-    bool ok = true;
-    while (ok && w.more()) {
-      Walk wn = w;
-      wn.next(p, TB);
-      const bool more = wn.more();
-      if (more) fetch_q(wn);
-      const int t = w.i * TB + tl;
+    uint32_t g0 = 0, nseg = 0;  // tiles and items before this one
+    for (Walk w(TB, start); w.more(); w.next(p, TB), ++nseg) {
+      const int t = w.i * TB + tl, n = w.n;
       const bool rvalid = tl < TB && t < w.s.nq;
+      if (nseg == 0 && wg == 0) {
+        fetch_q(row_of(w));
+        place_q();
+      }
       // local keys [0, seen) are visible to this row (rows that do not exist follow the last one)
       const int seen = w.s.len - w.s.nq + (rvalid ? t : min(w.i * TB + TB, w.s.nq) - 1) + 1;
-      float m_run = -INFINITY, l_run = 0.f;  // running max in the scaled log2 domain
-      for (int j = 0; j < w.n; ++j, ++g) {
+      // the owner of the item's last tile sees to the next item's Q
+      const bool next_q = ((g0 + n - 1) & 1) == (uint32_t)wg && w.f + n < w.f1;
+      const int j0 = (int)((g0 ^ wg) & 1);
+      float m = -INFINITY, l_run = 0.f;  // this warpgroup's reference maximum (a whole number) and row sum
+      for (int j = j0; j < n; j += 2) {
+        const uint32_t g = g0 + j;
         const int st = g & 1, tile = w.t0 + j;
         const bool mem = tile < w.s.nm;
         // a memory tile's segment counts (one byte per segment), loaded before the wait
         uint4 segc = make_uint4(0u, 0u, 0u, 0u);
         if (mem) segc = __ldg(reinterpret_cast<const uint4*>(a.seg_cnt + w.b * p.Smax + tile * kTileSegs));
-        // waits are decided warp-wide so the warp-collective tcgen05 ops are never split
-        if (!__all_sync(0xffffffffu, wait(&s_full[st], (g >> 1) & 1))) {
-          ok = false;
-          break;
-        }
+        hold(&s_full[st], (g >> 1) & 1);
         tc_fence_after();
+        if (next_q && j == j0) {
+          // this item's S has begun, so its Q has left the shared memory
+          Walk wn = w;
+          wn.next(p, TB);
+          fetch_q(row_of(wn));
+        }
+        if (next_q && j == n - 1) place_q();  // the item's last S is done: Q's columns are free
         float s[kKeys];
 #pragma unroll
-        for (int c = 0; c < kKeys; c += 16) tmem_ld16(tmem + lane_off + st * kKeys + c, *reinterpret_cast<float(*)[16]>(&s[c]));
+        for (int c = 0; c < kKeys; c += 16) tmem_ld16(tS0 + lane_off + st * kKeys + c, *reinterpret_cast<float(*)[16]>(&s[c]));
         tmem_ld_wait();
-        bool masked = false;  // some key of the tile is not visible to some row of the warp
+        tc_fence_before();
+        mbar_arrive(&s_free[st]);
         if (mem) {
           // key c of the tile is row c % kSegRows of segment c / kSegRows
           static_assert(kTileSegs == 16 && kSegRows == 8, "four segment counts per word");
           const uint32_t full8 = 0x08080808u;
-          masked = !(segc.x == full8 && segc.y == full8 && segc.z == full8 && segc.w == full8);
-          if (masked) {
+          if (!(segc.x == full8 && segc.y == full8 && segc.z == full8 && segc.w == full8)) {
             const uint32_t cw[4] = {segc.x, segc.y, segc.z, segc.w};
 #pragma unroll
             for (int c = 0; c < kKeys; ++c) {
-              const uint32_t n = (cw[c >> 5] >> (((c >> 3) & 3) * 8)) & 0xffu;
-              s[c] = (uint32_t)(c & 7) < n ? s[c] : -INFINITY;
+              const uint32_t cnt = (cw[c >> 5] >> (((c >> 3) & 3) * 8)) & 0xffu;
+              s[c] = (uint32_t)(c & 7) < cnt ? s[c] : -INFINITY;
             }
           }
         } else {
           const int base = (tile - w.s.nm) * kKeys;
           const int lim = seen - base;
-          masked = __any_sync(0xffffffffu, lim < kKeys);
-          if (masked) {
+          if (__any_sync(0xffffffffu, lim < kKeys)) {
 #pragma unroll
             for (int c = 0; c < kKeys; ++c) s[c] = c < lim ? s[c] : -INFINITY;
           }
-          // Rows of V past the sequence's end: zeros.  The copy that filled the stage has landed
-          // (S read the same barrier's K); this wait makes it visible to this thread.
+          // rows of V past the sequence's end: zeros, before this tile's PV
           const int end = w.s.len - base;
           if (end < kKeys) {
             const uint32_t vs = g % kKV;
-            if (!__all_sync(0xffffffffu, wait(&kv_full[vs], (g / kKV) & 1))) {
-              ok = false;
-              break;
-            }
+            hold(&v_full[vs], (g / kKV) & 1);
             if (r >= end) {
               uint8_t* v = Vs + vs * L::kK + r * 128;
 #pragma unroll
@@ -452,115 +461,133 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmKm, const __grid_cons
 #pragma unroll
         for (int i = 0; i < 8; ++i) m8[i] = fmaxf(m8[i], s[120 + i]);
         const float mx = fmaxf(fmax3(m8[0], m8[1], m8[2]), fmax3(fmax3(m8[3], m8[4], m8[5]), m8[6], m8[7]));
-        // move the max (and rescale O) only when it grows by more than 2^8
+        // the reference moves only when a score passes it by 2^8, to the next whole number: every
+        // later change of scale is then a power of two, exact in any type
         const float mt = mx * sl2;
-        const bool grow = mt > m_run + kRescaleLog2;
-        float corr = 1.f;
-        if (grow) {
-          corr = m_run == -INFINITY ? 0.f : fast_exp2(m_run - mt);
-          m_run = mt;
+        if (mt > m + kRescaleLog2) {
+          const float up = ceilf(mt);
+          l_run *= m == -INFINITY ? 0.f : fast_exp2(m - up);
+          m = up;
         }
-        if (j > 0 && __any_sync(0xffffffffu, grow)) {
-          // O must hold every earlier PV before it is rescaled
-          if (!__all_sync(0xffffffffu, wait(&p_free[(g - 1) & 1], ((g - 1) >> 1) & 1))) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-#pragma unroll
-          for (int c = 0; c < DH; c += 16) {
-            float o[16];
-            tmem_ld16(tO + lane_off + c, o);
-            tmem_ld_wait();
-            uint32_t wv[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) wv[i] = __float_as_uint(o[i] * corr);
-            tmem_st16(tO + lane_off + c, wv);
-          }
-          tmem_st_wait();
-        }
-        l_run *= corr;
-        const float nm = m_run == -INFINITY ? 0.f : -m_run;  // no key seen yet: 2^(-inf) below is 0
-        // P over S: 32 keys (16 columns of bf16 pairs) per store; the scaled arguments and the row
-        // sums in packed pairs (one f32x2 instruction for two keys).  Tiles with masked keys take
-        // ex2 throughout, which gives masked keys exactly 0.
+        const float nm = m == -INFINITY ? 0.f : -m;  // no key seen yet: 2^(-inf) below is 0
+        // P in registers (a pair of keys per word); the scaled arguments and the row sums in packed
+        // pairs (one f32x2 instruction for two keys).  All on the transcendental unit (1,024 cycles
+        // of its time a tile): with a share of the exponentials as polynomials on the FMA pipes the
+        // 4096-token part over 32,096 keys took 2.10 ms (2 of 16 pairs) to 2.29 ms (8), without
+        // 1.97 ms.
         const uint64_t sl2x2 = f2_pack(sl2, sl2), nmx2 = f2_pack(nm, nm);
         uint64_t lsa2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
-        auto weights = [&](auto poly) {
+        uint32_t pw[kKeys / 2];
 #pragma unroll
-          for (int c0 = 0; c0 < kKeys; c0 += 32) {
-            uint32_t wv[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float x0, x1, e0, e1;
-              f2_unpack(f2_fma(f2_pack(s[c0 + 2 * i], s[c0 + 2 * i + 1]), sl2x2, nmx2), x0, x1);
-              if (poly.value && poly_pair(i)) {
-                exp2_poly2(x0, x1, e0, e1);
-              } else {
-                e0 = fast_exp2(x0);
-                e1 = fast_exp2(x1);
-              }
-              lsa2[i & 1] = f2_add(lsa2[i & 1], f2_pack(e0, e1));
-              wv[i] = pack_bf16x2(e0, e1);
-            }
-            tmem_st16(tmem + lane_off + st * kKeys + c0 / 2, wv);
-          }
-        };
-        if (masked) weights(std::false_type{});
-        else weights(std::true_type{});
+        for (int i = 0; i < kKeys / 2; ++i) {
+          float x0, x1;
+          f2_unpack(f2_fma(f2_pack(s[2 * i], s[2 * i + 1]), sl2x2, nmx2), x0, x1);
+          const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
+          lsa2[i & 1] = f2_add(lsa2[i & 1], f2_pack(e0, e1));
+          pw[i] = pack_bf16x2(e0, e1);
+        }
         float lsa[4];
         f2_unpack(lsa2[0], lsa[0], lsa[1]);
         f2_unpack(lsa2[1], lsa[2], lsa[3]);
         l_run += (lsa[0] + lsa[1]) + (lsa[2] + lsa[3]);
+        // P goes into tensor memory once the PV of the tile before has read its own.  (A barrier of
+        // its own for even and odd tiles: with one, a warp two tiles ahead would take the phase
+        // before the last for the one it waits for.)
+        if (g > 0) {
+          hold(&p_free[(g - 1) & 1], ((g - 1) >> 1) & 1);
+        }
+        tc_fence_after();
+        // the reference that O has, as the owner of the tile before left it (before its arrival on
+        // p_full, which the PV behind p_free waited for).  Tiles publish in order, so this is the
+        // place where the two warpgroups' references meet.
+        const float ms = j > 0 ? m_s[r] : -INFINITY;
+        if (__any_sync(0xffffffffu, m != ms)) {
+          float fo = 1.f, fp = 1.f;  // factors of O and of P
+          if (m > ms) {
+            if (ms != -INFINITY) fo = fast_exp2(ms - m);  // else no key so far: O is 0 (or not begun)
+          } else if (m < ms) {
+            fp = m == -INFINITY ? 0.f : fast_exp2(m - ms);  // -inf: P is 0 already
+            l_run *= fp;
+            m = ms;
+          }
+          m_s[r] = m;
+          if (__any_sync(0xffffffffu, fo != 1.f)) {
+#pragma unroll 1
+            for (int c = 0; c < DH; c += 16) {
+              float o[16];
+              tmem_ld16(tO + lane_off + c, o);
+              tmem_ld_wait();
+              uint32_t wv[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) wv[i] = __float_as_uint(o[i] * fo);
+              tmem_st16(tO + lane_off + c, wv);
+            }
+          }
+          if (__any_sync(0xffffffffu, fp != 1.f)) {
+            const __nv_bfloat162 f2 = __float2bfloat162_rn(fp);
+#pragma unroll
+            for (int i = 0; i < kKeys / 2; ++i) {
+              __nv_bfloat162 v = *reinterpret_cast<__nv_bfloat162*>(&pw[i]);
+              v = __hmul2(v, f2);
+              pw[i] = *reinterpret_cast<uint32_t*>(&v);
+            }
+          }
+        }
+        if (j == 0) m_s[r] = m;
+#pragma unroll
+        for (int c = 0; c < kKeys / 2; c += 16) tmem_st16(tP + lane_off + c, *reinterpret_cast<const uint32_t(*)[16]>(&pw[c]));
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(&p_full[st]);
+        mbar_arrive(p_full);
       }
-      if (!ok) break;
-      // the next item's Q, so that its first S runs beside this item's output; its buffer was last
-      // read by the S MMAs of the item before this one
-      if (more) place_q(tQ0 + ((nseg + 1) & 1) * (DH / 2));
-      const uint32_t gl = g - 1;
-      if (!__all_sync(0xffffffffu, wait(&p_free[gl & 1], (gl >> 1) & 1))) {
-        ok = false;
-        break;
+      // The item's end belongs to the owner of its last tile; the other warpgroup leaves its sum and
+      // goes on to the next item, whose first tile is its own.
+      const uint32_t gl = g0 + n - 1;
+      g0 += n;
+      if ((int)(gl & 1) != wg) {
+        if (nseg > 0) hold(o_read, (nseg - 1) & 1);  // the last item's sum has been read
+        ml_s[r] = make_float2(m, l_run);
+        mbar_arrive(&l_ready[q]);
+        continue;
       }
+      hold(&l_ready[q], nseg & 1);
+      const float2 ml = ml_s[r];
+      // this warpgroup stored the last P, so its reference is O's, and no smaller than the other's
+      const float l = l_run + (ml.y == 0.f ? 0.f : ml.y * fast_exp2(ml.x - m));
+      hold(&p_free[gl & 1], (gl >> 1) & 1);
       tc_fence_after();
-      const bool whole = w.whole();
+      float o[DH];
+#pragma unroll
+      for (int c = 0; c < DH; c += 16) tmem_ld16(tO + lane_off + c, *reinterpret_cast<float(*)[16]>(&o[c]));
+      tmem_ld_wait();
+      tc_fence_before();
+      mbar_arrive(o_read);
       // O / l, lse = (m + log2 l) ln 2; the sum is 0 only for a row that saw no key: O = 0, lse = -inf
-      const bool none = l_run == 0.f;
-      const float inv = none ? 0.f : 1.f / l_run;
+      const bool none = l == 0.f, whole = w.whole();
+      const float inv = none ? 0.f : 1.f / l;
       const int64_t row = w.s.q0 + t;
       const int h = w.g * a.G + hh;
-      __nv_bfloat16* orow = a.O + (row * a.Hq + h) * DH;
-      float* slot = a.slots + slot_of(blockIdx.x, w.f, start->f0) * slot_floats(kRows, DH);
+      if (rvalid) {
+        if (whole) {
+          __nv_bfloat16* orow = a.O + (row * a.Hq + h) * DH;
 #pragma unroll
-      for (int c = 0; c < DH; c += 16) {
-        float o[16];
-        tmem_ld16(tO + lane_off + c, o);
-        tmem_ld_wait();
-        if (rvalid && whole) {
-#pragma unroll
-          for (int i = 0; i < 16; i += 8) {
+          for (int c = 0; c < DH; c += 8) {
             float f[8];
 #pragma unroll
-            for (int x = 0; x < 8; ++x) f[x] = none ? 0.f : o[i + x] * inv;
-            *reinterpret_cast<uint4*>(orow + c + i) = pack(f);
+            for (int x = 0; x < 8; ++x) f[x] = none ? 0.f : o[c + x] * inv;
+            *reinterpret_cast<uint4*>(orow + c) = pack(f);
           }
-        } else if (rvalid) {
+          if (a.lse) a.lse[(int64_t)h * p.N + row] = none ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+        } else {
+          float* slot = a.slots + slot_of(blockIdx.x, w.f, start->f0) * slot_floats(kRows, DH);
 #pragma unroll
-          for (int i = 0; i < 16; i += 4)
-            *reinterpret_cast<float4*>(slot + (((c + i) >> 2) * kRows + r) * 4) =
-                make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          for (int c = 0; c < DH; c += 4)
+            *reinterpret_cast<float4*>(slot + ((c >> 2) * kRows + r) * 4) =
+                make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+          *reinterpret_cast<float2*>(slot + kRows * DH + 2 * r) = make_float2(m, l);
         }
-        __syncwarp();
       }
-      if (rvalid) {
-        if (!whole) *reinterpret_cast<float2*>(slot + kRows * DH + 2 * r) = make_float2(m_run, l_run);
-        else if (a.lse) a.lse[(int64_t)h * p.N + row] = none ? -INFINITY : (m_run + log2f(l_run)) * 0.69314718055994531f;
-      }
-      ++nseg;
-      w = wn;
+      __syncwarp();
     }
   }
 
@@ -602,6 +629,7 @@ cudaError_t prefill_t(const PagedAttnArgs& a, cudaStream_t s) {
   d.G = G;
   d.TB = kRows / G;
   d.box_rows = box;
+  d.page_shift = __builtin_ctz((unsigned)a.p.page);
   d.O = reinterpret_cast<__nv_bfloat16*>(a.O);
   d.lse = a.lse;
   d.marks = reinterpret_cast<Mark*>(a.part);

@@ -7,7 +7,8 @@
 // All tiles of all items form one sequence f = 0 .. Ttot-1 (KV head outermost,
 // then sequence, block, tile), and CTA c takes the contiguous share
 // [c * per, (c + 1) * per), so every CTA streams the same number of tiles
-// whatever the lengths are.  A stretch of the share inside one item is a
+// whatever the lengths are; or, where there are no more items than CTAs and the
+// longest is at most `slack` tiles longer than that share, CTA c takes item c.  A stretch of the share inside one item is a
 // segment.  An item inside one CTA is finished there; an item cut by a share's
 // border leaves (row maxima, row sums, unnormalised rows) of each segment in
 // the workspace, merged by a second kernel in the order of the CTAs (no atomics:
@@ -110,65 +111,106 @@ __device__ __forceinline__ int64_t tiles_before(const Seq& s, int TB, int n) {
   return all ? t + block_tiles(s, TB, nb - 1) : t;
 }
 
+// Largest item of a sequence: its last block (the only ones with more keys come later).
+__device__ __forceinline__ int largest_item(const Seq& s, int TB) {
+  const int nb = (int)(((uint32_t)s.nq + TB - 1) / (uint32_t)TB);
+  return nb ? block_tiles(s, TB, nb - 1) : 0;
+}
+
 struct Start {            // where a CTA's share begins
   int64_t per, f0, f1;    // tiles per CTA, the share
   int64_t b;              // sequence, KV head, block and tile of f0
   Seq s;
   int g, i, t;
   int any;                // the share is not empty
-  int64_t rest;           // scan scratch: tile of the sequence, sums per warp
-  int64_t sums[16];
+  int one;                // the share is one whole item
+  int64_t rest;           // scratch: tile (or block) of the sequence
+};
+
+struct ScanScratch {  // shared memory, free again after find_start
+  int64_t sums[16];   // per warp
+  int counts[16], tops[16];
 };
 
 // All threads of the CTA call it (blockDim.x a multiple of 32, at most 512);
 // on return st (shared memory) holds share c of `grid` shares.
-__device__ __forceinline__ void find_start(const PagedBatch& p, int TB, int64_t c, int64_t grid, bool report,
-                                           Start* st) {
-  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
-  const int chunk = (int)((p.B + nt - 1) / nt);  // B < 2^31
+__device__ __forceinline__ void find_start(const PagedBatch& p, int TB, int slack, int64_t c, int64_t grid,
+                                           bool report, Start* st, ScanScratch* sc) {
+  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = nt >> 5;
+  const int chunk = (int)(((uint32_t)p.B + nt - 1) / (uint32_t)nt);  // B < 2^31
   const int64_t b0 = min(p.B, (int64_t)tid * chunk), b1 = min(p.B, b0 + chunk);
-  int64_t mine = 0;
+  int64_t mine = 0;   // tiles of this thread's sequences
+  int items = 0, most = 0;  // their blocks (at most N < 2^31), the largest of them
   Seq s;
   for (int64_t b = b0; b < b1; ++b) {
     s = load_seq(p, b, report ? p.err_flag : nullptr);
     mine += tiles_before(s, TB, 0x7fffffff);
+    items += (int)(((uint32_t)s.nq + TB - 1) / (uint32_t)TB);
+    most = max(most, largest_item(s, TB));
   }
+  // only the first warps have sequences when there are few: the others' sums are 0
+  const int used = (int)min((int64_t)warps, (p.B + 31 * (int64_t)chunk) / (32 * (int64_t)chunk) + 1);
   int64_t incl = mine;
+  int icl = items;
+  if (warp < used) {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+      const int u = __shfl_up_sync(0xffffffffu, icl, o);
+      if (lane >= o) {
+        incl += v;
+        icl += u;
+      }
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 31) {
+      sc->sums[warp] = incl;
+      sc->counts[warp] = icl;
+      sc->tops[warp] = most;
+    }
   }
-  if (lane == 31) st->sums[warp] = incl;
   __syncthreads();
   int64_t before = 0, total = 0;
-  for (int w = 0; w < (nt >> 5); ++w) {
-    if (w < warp) before += st->sums[w];
-    total += st->sums[w];
+  int ibefore = 0, n_items = 0;
+  most = 0;
+  for (int w = 0; w < used; ++w) {
+    if (w < warp) {
+      before += sc->sums[w];
+      ibefore += sc->counts[w];
+    }
+    total += sc->sums[w];
+    n_items += sc->counts[w];
+    most = max(most, sc->tops[w]);
   }
   incl += before;
+  icl += ibefore;
   const int64_t Ttot = total * p.Hkv;
   // 32-bit divisions where the numbers allow (64-bit ones cost about a microsecond together)
   const bool small = Ttot + grid < 0x7fffffff;
   const int64_t per = max((int64_t)1, small ? (int64_t)((uint32_t)(Ttot + grid - 1) / (uint32_t)grid)
                                             : (Ttot + grid - 1) / grid);
-  const int64_t f0 = c * per, f1 = min(f0 + per, Ttot);
-  const bool any = f0 < f1;
-  const int64_t g = !any ? 0 : small ? (int64_t)((uint32_t)f0 / (uint32_t)total) : f0 / total;
+  const bool one = (int64_t)n_items * p.Hkv <= grid && most <= per + slack;  // an item per CTA
+  const int64_t f0 = c * per;
+  const bool any = one ? c < (int64_t)n_items * p.Hkv : f0 < Ttot;
+  // KV head, and the tile (or block) of that head where the share begins
+  const int64_t div = one ? n_items : total, at = one ? c : f0;
+  const int64_t g = !any ? 0 : small ? (int64_t)((uint32_t)at / (uint32_t)div) : at / div;
+  const int64_t w = at - g * div;
   if (tid == 0) {
     st->per = per;
-    st->f0 = f0;
-    st->f1 = f1;
+    st->f0 = one ? 0 : f0;
+    if (!one) st->f1 = min(f0 + per, Ttot);
     st->any = any;
+    st->one = one;
     st->g = (int)g;
   }
-  const int64_t w = f0 - g * total;
-  if (any && w >= incl - mine && w < incl) {  // exactly one thread
-    int64_t rest = w - (incl - mine), b = b0;
+  const int64_t lo_w = one ? icl - items : incl - mine, hi_w = one ? icl : incl;
+  if (any && w >= lo_w && w < hi_w) {  // exactly one thread
+    int64_t rest = w - lo_w, b = b0;
     if (chunk > 1) {
       for (;;) {
         s = load_seq(p, b);
-        const int64_t n = tiles_before(s, TB, 0x7fffffff);
+        const int64_t n = one ? (int64_t)(((uint32_t)s.nq + TB - 1) / (uint32_t)TB) : tiles_before(s, TB, 0x7fffffff);
         if (rest < n) break;
         rest -= n;
         ++b;
@@ -177,27 +219,34 @@ __device__ __forceinline__ void find_start(const PagedBatch& p, int TB, int64_t 
     st->b = b;
     st->s = s;
     st->rest = rest;
-  }
-  __syncthreads();
-  if (any && warp == 0) {
-    // the block holding tile `rest`: the last one with tiles_before(block) <= rest, 32 probes at a time
-    const Seq q = st->s;
-    const int64_t rest = st->rest;
-    int lo = 0, n = (int)(((uint32_t)q.nq + TB - 1) / (uint32_t)TB);  // answer in [lo, lo + n)
-    while (n > 1) {
-      const int step = (n + 31) >> 5;
-      const int at = lo + lane * step;
-      const unsigned hit = __ballot_sync(0xffffffffu, lane * step < n && tiles_before(q, TB, at) <= rest);
-      const int last = 31 - __clz(hit);  // lane 0 always hits
-      lo += last * step;
-      n = min(step, n - last * step);
-    }
-    if (lane == 0) {
-      st->i = lo;
-      st->t = (int)(rest - tiles_before(q, TB, lo));
+    if (one) {
+      st->i = (int)rest;
+      st->t = 0;
+      st->f1 = block_tiles(s, TB, (int)rest);
     }
   }
   __syncthreads();
+  if (any && !one) {
+    if (warp == 0) {
+      // the block holding tile `rest`: the last one with tiles_before(block) <= rest, 32 probes at a time
+      const Seq q = st->s;
+      const int64_t rest = st->rest;
+      int lo = 0, n = (int)(((uint32_t)q.nq + TB - 1) / (uint32_t)TB);  // answer in [lo, lo + n)
+      while (n > 1) {
+        const int step = (n + 31) >> 5;
+        const int probe = lo + lane * step;
+        const unsigned hit = __ballot_sync(0xffffffffu, lane * step < n && tiles_before(q, TB, probe) <= rest);
+        const int last = 31 - __clz(hit);  // lane 0 always hits
+        lo += last * step;
+        n = min(step, n - last * step);
+      }
+      if (lane == 0) {
+        st->i = lo;
+        st->t = (int)(rest - tiles_before(q, TB, lo));
+      }
+    }
+    __syncthreads();
+  }
 }
 
 // Walks a CTA's share segment by segment.

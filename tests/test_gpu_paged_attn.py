@@ -99,6 +99,16 @@ def test_long_caches(dtype, q_len, total, Hq, Hkv, d):
     b.check(O, lse)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_single_tokens_in_a_batch_with_parts(d):
+    """Long runs of tiles where most rows of a block do not exist (their warps run ahead)."""
+    b = Batch([1, 40, 1, 2, 1], [20001, 300, 20001, 16000, 9000], 8, 4, d, 128, BF, DEV, seed=19)
+    for _ in range(3):
+        O, lse, flag = b.run()
+        assert _flag(flag) == 0
+    b.check(O, lse)
+
+
 def test_many_sequences():
     """More sequences than threads that plan the split, most of them tiny, some without new tokens."""
     g = torch.Generator().manual_seed(7)
