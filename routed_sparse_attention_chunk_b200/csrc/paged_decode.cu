@@ -15,9 +15,9 @@
 // it grows by more than 2^8; weights are rounded to bf16 for the P V product
 // (2^-9 each, averaged over the keys), their sum is kept from the fp32 values.
 // A tile's K and V arrive as one box per page (128 rows from pages of 128 and
-// more), one lane each, straight from the block table's pages; rows past the
-// sequence's end are never visible, and its V rows are zeroed in shared memory
-// before the product, because 0 x NaN is NaN and a page's tail holds anything.
+// more), one lane each, straight from the block table's pages (paged_tma.cuh); rows
+// past the sequence's end are never visible, and their V rows are zeroed in shared
+// memory before the product.
 // The split over CTAs is that of paged_sched.cuh: one CTA per SM, equal shares.
 // Warp roles (192 threads): warp 0 TMA producer, warp 1 TMEM owner + MMA
 // issuer, warps 2..5 softmax / output.  Every wait is bounded; after the first
@@ -26,6 +26,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "paged_sched.cuh"
+#include "paged_tma.cuh"
 #include "sm100.cuh"
 #include "tma_host.h"
 
@@ -51,7 +52,7 @@ struct DecParams {
   const int32_t* seg_row;
   const uint8_t* seg_cnt;
   int Hq, G, R;      // R = G * max_q
-  int box_rows;      // rows of one box: min(page, 128)
+  PageMap pm;
   __nv_bfloat16* O;
   float* lse;
   Mark* marks;
@@ -60,7 +61,7 @@ struct DecParams {
 };
 
 struct DLayout {
-  static constexpr int kTile = kKeys * kDH * 2;       // one K (or V) tile, two 64-wide boxes
+  static constexpr int kTile = Tile<kDH>::kBytes;     // one K (or V) tile
   static constexpr int kStage = 2 * kTile;
   static constexpr int kQ = kMaxRows * kDH * 2;       // Q rows, K-major, 128-byte swizzle (two buffers)
   static constexpr int kP = kMaxRows * kKeys * 2;     // P^T rows (query rows x keys); two buffers
@@ -104,8 +105,7 @@ __device__ __forceinline__ int sw128_off(int row, int col, int rows) {
 // the MMA's N stays 16 and the columns past kR are never read.
 template <int kR>
 __global__ void __launch_bounds__(kThreads, 1)
-paged_decode_kernel(const __grid_constant__ CUtensorMap tmKm, const __grid_constant__ CUtensorMap tmVm,
-                    const __grid_constant__ CUtensorMap tmKl, const __grid_constant__ CUtensorMap tmVl, DecParams a) {
+paged_decode_kernel(const __grid_constant__ TileMaps maps, DecParams a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* ring = smem;
@@ -164,61 +164,39 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmKm, const __grid_const
 
   if (warp == 0) {
     // ---------------------------------------------------------------- producer
-    // Lane 0 waits and arms the barriers.  A tile is up to 16 boxes per 64-column
-    // half of K and of V, one lane each: the plan's segments of kSegRows bank rows,
-    // or the pages (parts of pages) that hold cached tokens.  Each lands on a 1 KB
-    // swizzle atom, so the tile's layout is that of one 128-row box.
+    // Lane 0 waits and arms the barriers.  A tile is up to 16 boxes of K and of V, one lane
+    // each: the plan's segments of kSegRows bank rows, or the pages (parts of pages) that hold
+    // cached tokens.  A lane's place in the block table is looked up one tile ahead.
     uint32_t it = 0;
     bool stop = false;
+    auto locate = [&](const Walk& w, int t) {
+      return locate_box(p, a.pm, a.seg_row, w.b, w.s.nm, w.s.len, t, lane);
+    };
     for (Walk w(TB, start); w.more() && !stop; w.next(p, TB)) {
+      Box x = locate(w, w.t0);
       for (int t = w.t0; t < w.t0 + w.n; ++t, ++it) {
-        const uint32_t st = it % kStages, round = it / kStages;
+        const uint32_t st = it % kStages;
         const bool mem = t < w.s.nm;
-        const int key0 = mem ? 0 : (t - w.s.nm) * kKeys;
-        const int rows = mem ? kSegRows : a.box_rows;
-        // this lane's box: bank row, or page and row inside it
-        bool mine;
-        int at = 0, in_page = 0;
-        if (mem) {
-          mine = lane < kTileSegs;
-          if (mine) at = __ldg(a.seg_row + w.b * p.Smax + t * kTileSegs + lane);
-        } else {
-          const int k = key0 + lane * rows;
-          mine = lane * rows < kKeys && k < w.s.len;
-          if (mine) {
-            const int pi = k / p.page;
-            in_page = k - pi * p.page;
-            at = __ldg(p.table + w.b * p.max_pages + pi);
-            if (at < 0 || at >= p.num_pages) {  // read as zeros (a page past the last)
-              raise_flag(p.err_flag, MSA_FLAG_INDEX_OOB);
-              at = (int)p.num_pages;
-            }
-          }
-        }
-        const int boxes = __popc(__ballot_sync(0xffffffffu, mine));
+        const int rows = mem ? kSegRows : a.pm.box_rows;
+        check_box(p, mem, &x);
+        Box nx{false, 0, 0};
+        if (t + 1 < w.t0 + w.n) nx = locate(w, t + 1);
+        const int boxes = __popc(__ballot_sync(0xffffffffu, x.mine));
         int ok = 1;
         if (lane == 0) {
-          ok = mbar_wait_or_stop(&kv_empty[st], (round & 1) ^ 1, kWaitPolls, abort_s);
+          ok = mbar_wait_or_stop(&kv_empty[st], ((it / kStages) & 1) ^ 1, kWaitPolls, abort_s);
           if (ok) mbar_arrive_expect_tx(&kv_full[st], (uint32_t)(boxes * rows * kDH * 2 * 2));
         }
         if (!__shfl_sync(0xffffffffu, ok, 0)) {
           stop = true;
           break;
         }
-        if (mine) {
-          uint8_t* Kd = ring + st * DLayout::kStage + lane * (rows * 128);
-          uint8_t* Vd = Kd + DLayout::kTile;
-#pragma unroll
-          for (int dc = 0; dc < 2; ++dc) {
-            if (mem) {
-              tma_load_2d(Kd + dc * (kKeys * 128), &tmKm, w.g * kDH + dc * 64, at, &kv_full[st]);
-              tma_load_2d(Vd + dc * (kKeys * 128), &tmVm, w.g * kDH + dc * 64, at, &kv_full[st]);
-            } else {
-              tma_load_4d(Kd + dc * (kKeys * 128), &tmKl, dc * 64, w.g, in_page, at, &kv_full[st]);
-              tma_load_4d(Vd + dc * (kKeys * 128), &tmVl, dc * 64, w.g, in_page, at, &kv_full[st]);
-            }
-          }
+        if (x.mine) {
+          uint8_t* Kd = ring + st * DLayout::kStage;
+          load_box<kDH>(Kd, &maps.k, &maps.kbar, a.pm, mem, x, w.g, lane, &kv_full[st]);
+          load_box<kDH>(Kd + DLayout::kTile, &maps.v, &maps.vbar, a.pm, mem, x, w.g, lane, &kv_full[st]);
         }
+        x = nx;
       }
     }
     if (lane == 0) {
@@ -256,7 +234,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmKm, const __grid_const
 #pragma unroll
               for (int k = 0; k < kDH / 16; ++k) {
                 const int box = k >> 2, kk = k & 3;
-                mma_bf16_ss(tS + sb * 16, desc_k_sw128(k0 + box * (kKeys * 128) + kk * 32),
+                mma_bf16_ss(tS + sb * 16, desc_k_sw128_sbo(k0 + box * 1024 + kk * 32, Tile<kDH>::kGroup),
                             desc_k_sw128(q0 + box * (kMaxRows * 128) + kk * 32), idS, k > 0 ? 1u : 0u);
               }
               mma_commit(&s_full[sb]);
@@ -273,7 +251,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmKm, const __grid_const
 #pragma unroll
               for (int k = 0; k < kKeys / 16; ++k) {
                 const int box = k >> 2, kk = k & 3;
-                mma_bf16_ss(tO, desc_mn_sw128(v0 + k * 16 * 128, kKeys * 128),
+                mma_bf16_ss(tO, desc_mn_sw128_sbo(v0 + k * 2 * Tile<kDH>::kGroup, 1024, Tile<kDH>::kGroup),
                             desc_k_sw128(pp + box * (kMaxRows * 128) + kk * 32), idO, (nP > 0 || k > 0) ? 1u : 0u);
               }
               mma_commit(&o_done[pb]);
@@ -373,12 +351,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmKm, const __grid_const
         if (!mem && w.s.len - (key - r_lane) < kKeys) {
           const uint32_t st = g % kStages;
           hold(&kv_full[st], (g / kStages) & 1);
-          if (key >= w.s.len) {
-            uint8_t* v = ring + st * DLayout::kStage + DLayout::kTile + r_lane * 128;
-#pragma unroll
-            for (int c = 0; c < 16; ++c)
-              *reinterpret_cast<uint4*>(v + (c >> 3) * (kKeys * 128) + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-          }
+          if (key >= w.s.len) zero_row<kDH>(ring + st * DLayout::kStage + DLayout::kTile, r_lane);
           __syncwarp();
         }
         // The maximum moves only where a score passes it by 2^8 (always in the first tile with a
@@ -500,24 +473,10 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmKm, const __grid_const
 }  // namespace
 
 cudaError_t launch_paged_decode(const PagedAttnArgs& a, cudaStream_t s) {
-  CUtensorMap tkm, tvm, tkl, tvl;
-  const int box = a.p.page < kKeys ? a.p.page : kKeys;
-  const bool bank = a.Kbar != nullptr;
-  if (!make_tmap_pages_bf16(&tkl, a.K, kDH, a.p.Hkv, a.p.page, a.p.num_pages, a.head_stride, a.row_stride,
-                            a.page_stride, box) ||
-      !make_tmap_pages_bf16(&tvl, a.V, kDH, a.p.Hkv, a.p.page, a.p.num_pages, a.head_stride, a.row_stride,
-                            a.page_stride, box))
-    return cudaErrorInvalidValue;
-  tkm = tkl;  // never read without a plan
-  tvm = tvl;
-  if (bank) {
-    const uint64_t rowkv = (uint64_t)a.p.Hkv * kDH * 2;
-    if (!make_tmap_2d_bf16(&tkm, a.Kbar, (uint64_t)a.p.Hkv * kDH, (uint64_t)a.C, rowkv, 64, kSegRows) ||
-        !make_tmap_2d_bf16(&tvm, a.Vbar, (uint64_t)a.p.Hkv * kDH, (uint64_t)a.C, rowkv, 64, kSegRows))
-      return cudaErrorInvalidValue;
-  }
-  const int grid = sm_count(), G = a.Hq / a.p.Hkv;
+  TileMaps maps;
   DecParams d;
+  if (!make_tile_maps<kDH>(a, &maps, &d.pm)) return cudaErrorInvalidValue;
+  const int grid = sm_count(), G = a.Hq / a.p.Hkv;
   d.p = a.p;
   d.Q = reinterpret_cast<const __nv_bfloat16*>(a.Q);
   d.q_ts = a.q_ts;
@@ -526,7 +485,6 @@ cudaError_t launch_paged_decode(const PagedAttnArgs& a, cudaStream_t s) {
   d.Hq = a.Hq;
   d.G = G;
   d.R = G * a.p.max_q;
-  d.box_rows = box;
   d.O = reinterpret_cast<__nv_bfloat16*>(a.O);
   d.lse = a.lse;
   d.marks = reinterpret_cast<Mark*>(a.part);
@@ -537,7 +495,7 @@ cudaError_t launch_paged_decode(const PagedAttnArgs& a, cudaStream_t s) {
   cudaError_t e = allow_smem(kern, DLayout::kSmem, done[d.R <= 4 ? 0 : (d.R <= 8 ? 1 : 2)]);
   if (e != cudaSuccess) return e;
   count_launch();
-  e = launch_pdl(kern, dim3((unsigned)grid), dim3(kThreads), (size_t)DLayout::kSmem, s, tkm, tvm, tkl, tvl, d);
+  e = launch_pdl(kern, dim3((unsigned)grid), dim3(kThreads), (size_t)DLayout::kSmem, s, maps, d);
   if (e != cudaSuccess) return e;
   MergeArgs m{d.marks, d.slots, a.p.N, d.R, G, a.Hq, 1.f, a.O, a.lse};
   return launch_merge(MSA_BF16, kDH, false, m, grid, s);

@@ -19,11 +19,9 @@
 // the two are added under O's reference at the item's end, so the result is exact.
 // A row that has seen no key yet keeps the reference -inf and weights of 0.
 // A tile's K and V arrive as one box per page, straight from the block table's
-// pages, or per run of bank rows of the segment plan, K and V from a warp each
-// (small boxes: the issue rate of one warp was 3,600 cycles a tile for pages of
-// 16), in rings of three.  Rows past the sequence's end are masked, and their V
-// rows zeroed in shared memory before the product (0 x NaN is NaN, and a page's
-// tail holds anything).
+// pages, or per run of bank rows of the segment plan (paged_tma.cuh), K and V from a
+// warp each, in rings of three.  Rows past the sequence's end are masked, and their
+// V rows zeroed in shared memory before the product.
 // Persistent: one CTA per SM walks its equal share of all (item, tile) pairs
 // (paged_sched.cuh).  The pipeline runs through item borders: the next item's Q
 // rows wait in shared memory, and move to tensor memory as soon as the current
@@ -37,6 +35,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "paged_sched.cuh"
+#include "paged_tma.cuh"
 #include "sm100.cuh"
 #include "tma_host.h"
 
@@ -60,8 +59,7 @@ struct PreParams {
   const int32_t* seg_row;
   const uint8_t* seg_cnt;
   int Hq, G, TB;
-  int box_rows;  // rows of one box: min(page, 128)
-  int page_shift;
+  PageMap pm;
   __nv_bfloat16* O;
   float* lse;
   Mark* marks;
@@ -72,9 +70,8 @@ struct PreParams {
 template <int DH>
 struct Layout {
   static constexpr int kKV = 3;                // stages of the K ring and of the V ring
-  static constexpr int kBoxes = DH / 64;
   static constexpr int kQ = kRows * DH * 2;    // the next item's query rows on their way to tensor memory
-  static constexpr int kK = kKeys * DH * 2;    // one K (or V) tile
+  static constexpr int kK = Tile<DH>::kBytes;  // one K (or V) tile
   static constexpr int kBars = 30;
   static constexpr int kRowState = kRows * 4 + kRows * 8;  // O's references; one warpgroup's (reference, sum)
   static constexpr int kSmem = 1024 + kQ + 2 * kKV * kK + 8 * kBars + kRowState + (int)sizeof(Start);
@@ -124,8 +121,7 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
 
 template <int DH>
 __global__ void __launch_bounds__(kThreads, 1)
-paged_prefill_kernel(const __grid_constant__ CUtensorMap tmKm, const __grid_constant__ CUtensorMap tmVm,
-                     const __grid_constant__ CUtensorMap tmKl, const __grid_constant__ CUtensorMap tmVl, PreParams a) {
+paged_prefill_kernel(const __grid_constant__ TileMaps maps, PreParams a) {
   using L = Layout<DH>;
   constexpr int kKV = L::kKV;
   extern __shared__ uint8_t smem_raw[];
@@ -200,36 +196,17 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmKm, const __grid_cons
     setmaxnreg_dec<kOtherRegs>();
     if (warp == 0 || warp == 3) {
       // -------------------------------------------------------------- K and V producers
-      // Lane 0 waits and arms the barriers.  A tile is up to 16 boxes per 64-column
-      // half, one lane each: the plan's segments of kSegRows bank rows, or the pages
-      // (parts of pages) that hold cached tokens.  Each lands on a 1 KB swizzle atom,
-      // so the tile's layout is that of one 128-row box.  A lane's place in the block
-      // table is looked up one tile ahead.
+      // Lane 0 waits and arms the barriers.  A tile is up to 16 boxes, one lane each: the
+      // plan's segments of kSegRows bank rows, or the pages (parts of pages) that hold
+      // cached tokens.  A lane's place in the block table is looked up one tile ahead.
       const bool isK = warp == 0;
       uint8_t* ring = isK ? Ks : Vs;
       uint64_t* full = isK ? k_full : v_full;
       uint64_t* empty = isK ? k_empty : v_empty;
-      const CUtensorMap* mapm = isK ? &tmKm : &tmVm;
-      const CUtensorMap* mapl = isK ? &tmKl : &tmVl;
-      struct Box {
-        bool mine;
-        int at, in_page;  // bank row, or page and row inside it
-      };
+      const CUtensorMap* pages = isK ? &maps.k : &maps.v;
+      const CUtensorMap* bank = isK ? &maps.kbar : &maps.vbar;
       auto locate = [&](const Walk& w, int t) {
-        Box x{false, 0, 0};
-        if (t < w.s.nm) {
-          x.mine = lane < kTileSegs;
-          if (x.mine) x.at = __ldg(a.seg_row + w.b * p.Smax + t * kTileSegs + lane);
-        } else {
-          const int k = (t - w.s.nm) * kKeys + lane * a.box_rows;
-          x.mine = lane * a.box_rows < kKeys && k < w.s.len;
-          if (x.mine) {
-            const int pi = k >> a.page_shift;
-            x.in_page = k - (pi << a.page_shift);
-            x.at = __ldg(p.table + w.b * p.max_pages + pi);
-          }
-        }
-        return x;
+        return locate_box(p, a.pm, a.seg_row, w.b, w.s.nm, w.s.len, t, lane);
       };
       uint32_t it = 0;
       bool stop = false;
@@ -238,11 +215,8 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmKm, const __grid_cons
         for (int t = w.t0; t < w.t0 + w.n; ++t, ++it) {
           const uint32_t st = it % kKV;
           const bool mem = t < w.s.nm;
-          const int rows = mem ? kSegRows : a.box_rows;
-          if (!mem && x.mine && (x.at < 0 || x.at >= p.num_pages)) {  // read as zeros (a page past the last)
-            raise_flag(p.err_flag, MSA_FLAG_INDEX_OOB);
-            x.at = (int)p.num_pages;
-          }
+          const int rows = mem ? kSegRows : a.pm.box_rows;
+          check_box(p, mem, &x);
           Box nx{false, 0, 0};
           if (t + 1 < w.t0 + w.n) nx = locate(w, t + 1);
           const int boxes = __popc(__ballot_sync(0xffffffffu, x.mine));
@@ -255,14 +229,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmKm, const __grid_cons
             stop = true;
             break;
           }
-          if (x.mine) {
-            uint8_t* dst = ring + st * L::kK + lane * (rows * 128);
-#pragma unroll
-            for (int dc = 0; dc < L::kBoxes; ++dc) {
-              if (mem) tma_load_2d(dst + dc * (kKeys * 128), mapm, w.g * DH + dc * 64, x.at, &full[st]);
-              else tma_load_4d(dst + dc * (kKeys * 128), mapl, dc * 64, w.g, x.in_page, x.at, &full[st]);
-            }
-          }
+          if (x.mine) load_box<DH>(ring + st * L::kK, pages, bank, a.pm, mem, x, w.g, lane, &full[st]);
           x = nx;
         }
       }
@@ -278,7 +245,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmKm, const __grid_cons
         // descriptors of the operand bases; a k-step adds its byte offset / 16 to
         // the 14-bit start-address field (shared addresses stay below 256 KB, so
         // the field never carries)
-        const uint64_t dk0 = desc_k_sw128(smem_u32(Ks));
+        const uint64_t dk0 = desc_k_sw128_sbo(smem_u32(Ks), Tile<DH>::kGroup);
         uint32_t g = 0, nseg = 0;
         bool ok = true;
         for (Walk w(TB, start); ok && w.more(); w.next(p, TB), ++nseg) {
@@ -293,7 +260,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmKm, const __grid_cons
             for (int k = 0; k < DH / 16; ++k) {
               // A = Q from TMEM (16 elements of bf16 per step are 8 columns), B = K from its tile
               const int box = k >> 2, kk = k & 3;
-              mma_bf16_ts(tS0 + (g & 1) * kKeys, tQ + k * 8, dk + (uint64_t)((box * kKeys * 128 + kk * 32) >> 4), idS,
+              mma_bf16_ts(tS0 + (g & 1) * kKeys, tQ + k * 8, dk + (uint64_t)((box * 1024 + kk * 32) >> 4), idS,
                           k > 0 ? 1u : 0u);
             }
             mma_commit(&s_full[g & 1]);
@@ -307,7 +274,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmKm, const __grid_cons
       // -------------------------------------------------------------- PV issuer
       if (lane == 0) {
         constexpr uint32_t idO = idesc_bf16_f32(kRows, DH, /*b_mn_major=*/true);
-        const uint64_t dv0 = desc_mn_sw128(smem_u32(Vs), kKeys * 128);
+        const uint64_t dv0 = desc_mn_sw128_sbo(smem_u32(Vs), 1024, Tile<DH>::kGroup);
         uint32_t g = 0, nseg = 0;
         bool ok = true;
         for (Walk w(TB, start); ok && w.more(); w.next(p, TB), ++nseg) {
@@ -321,7 +288,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmKm, const __grid_cons
             // A = P from TMEM: 16 keys of bf16 per step are 8 columns
 #pragma unroll
             for (int k = 0; k < kKeys / 16; ++k)
-              mma_bf16_ts(tO, tP + k * 8, dv + (uint64_t)((k * 16 * 128) >> 4), idO, (j > 0 || k > 0) ? 1u : 0u);
+              mma_bf16_ts(tO, tP + k * 8, dv + (uint64_t)((k * 2 * Tile<DH>::kGroup) >> 4), idO, (j > 0 || k > 0) ? 1u : 0u);
             mma_commit(&p_free[g & 1]);
             mma_commit(&v_empty[vs]);
           }
@@ -439,12 +406,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmKm, const __grid_cons
           if (end < kKeys) {
             const uint32_t vs = g % kKV;
             hold(&v_full[vs], (g / kKV) & 1);
-            if (r >= end) {
-              uint8_t* v = Vs + vs * L::kK + r * 128;
-#pragma unroll
-              for (int c = 0; c < 8 * L::kBoxes; ++c)
-                *reinterpret_cast<uint4*>(v + (c >> 3) * (kKeys * 128) + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-            }
+            if (r >= end) zero_row<DH>(Vs + vs * L::kK, r);
             fence_async_smem();
             __syncwarp();
           }
@@ -603,23 +565,10 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tmKm, const __grid_cons
 template <int DH>
 cudaError_t prefill_t(const PagedAttnArgs& a, cudaStream_t s) {
   using L = Layout<DH>;
-  CUtensorMap tkm, tvm, tkl, tvl;
-  const int box = a.p.page < kKeys ? a.p.page : kKeys;
-  if (!make_tmap_pages_bf16(&tkl, a.K, DH, a.p.Hkv, a.p.page, a.p.num_pages, a.head_stride, a.row_stride,
-                            a.page_stride, box) ||
-      !make_tmap_pages_bf16(&tvl, a.V, DH, a.p.Hkv, a.p.page, a.p.num_pages, a.head_stride, a.row_stride,
-                            a.page_stride, box))
-    return cudaErrorInvalidValue;
-  tkm = tkl;  // never read without a plan
-  tvm = tvl;
-  if (a.Kbar) {
-    const uint64_t rowkv = (uint64_t)a.p.Hkv * DH * 2;
-    if (!make_tmap_2d_bf16(&tkm, a.Kbar, (uint64_t)a.p.Hkv * DH, (uint64_t)a.C, rowkv, 64, kSegRows) ||
-        !make_tmap_2d_bf16(&tvm, a.Vbar, (uint64_t)a.p.Hkv * DH, (uint64_t)a.C, rowkv, 64, kSegRows))
-      return cudaErrorInvalidValue;
-  }
-  const int grid = sm_count(), G = a.Hq / a.p.Hkv;
+  TileMaps maps;
   PreParams d;
+  if (!make_tile_maps<DH>(a, &maps, &d.pm)) return cudaErrorInvalidValue;
+  const int grid = sm_count(), G = a.Hq / a.p.Hkv;
   d.p = a.p;
   d.Q = reinterpret_cast<const __nv_bfloat16*>(a.Q);
   d.q_ts = a.q_ts;
@@ -628,8 +577,6 @@ cudaError_t prefill_t(const PagedAttnArgs& a, cudaStream_t s) {
   d.Hq = a.Hq;
   d.G = G;
   d.TB = kRows / G;
-  d.box_rows = box;
-  d.page_shift = __builtin_ctz((unsigned)a.p.page);
   d.O = reinterpret_cast<__nv_bfloat16*>(a.O);
   d.lse = a.lse;
   d.marks = reinterpret_cast<Mark*>(a.part);
@@ -639,8 +586,7 @@ cudaError_t prefill_t(const PagedAttnArgs& a, cudaStream_t s) {
   cudaError_t e = allow_smem(paged_prefill_kernel<DH>, L::kSmem, done);
   if (e != cudaSuccess) return e;
   count_launch();
-  e = launch_pdl(paged_prefill_kernel<DH>, dim3((unsigned)grid), dim3(kThreads), (size_t)L::kSmem, s, tkm, tvm, tkl,
-                 tvl, d);
+  e = launch_pdl(paged_prefill_kernel<DH>, dim3((unsigned)grid), dim3(kThreads), (size_t)L::kSmem, s, maps, d);
   if (e != cudaSuccess) return e;
   MergeArgs m{d.marks, d.slots, a.p.N, kRows, G, a.Hq, 1.f, a.O, a.lse};
   return launch_merge(MSA_BF16, DH, true, m, grid, s);

@@ -83,12 +83,20 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
-// 4D tiled load of the box at (x, y, z, w), x innermost.
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
-                                            int32_t w, uint64_t* bar) {
+// 3D and 5D tiled loads of the box at the given coordinates, innermost first.
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int32_t c0, int32_t c1, int32_t c2,
+                                            uint64_t* bar) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
-      ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+      ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, int32_t c0, int32_t c1, int32_t c2,
+                                            int32_t c3, int32_t c4, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
+      ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4),
+      "r"(smem_u32(bar))
       : "memory");
 }
 
@@ -247,6 +255,14 @@ __device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t smem_addr, uint32_t l
   d |= (uint64_t)1u << 46;
   d |= (uint64_t)2u << 61;
   return d;
+}
+
+// The same two descriptors for tiles whose groups of 8 rows lie `sbo` bytes apart.
+__device__ __forceinline__ uint64_t desc_k_sw128_sbo(uint32_t smem_addr, uint32_t sbo) {
+  return (desc_k_sw128(smem_addr) & ~((uint64_t)0x3fffu << 32)) | (uint64_t)(sbo >> 4) << 32;
+}
+__device__ __forceinline__ uint64_t desc_mn_sw128_sbo(uint32_t smem_addr, uint32_t lbo, uint32_t sbo) {
+  return (desc_mn_sw128(smem_addr, lbo) & ~((uint64_t)0x3fffu << 32)) | (uint64_t)(sbo >> 4) << 32;
 }
 
 // ------------------------------------------------------------------ CTA pairs (cta_group::2)

@@ -15,12 +15,10 @@ namespace msa {
 bool make_tmap_2d_bf16(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t row_bytes,
                        uint32_t box_inner, uint32_t box_outer);
 
-// 4D bf16 tensor map over the pages of a cache: element (x, head, row, page) at
-// x + head * head_stride + row * row_stride + page * page_stride (strides in
-// elements); box = box_rows rows of 64 elements of one head of one page, 128-byte
-// swizzle, pages past the last read as zero.  False if the driver rejects it.
-bool make_tmap_pages_bf16(CUtensorMap* map, const void* base, int d, int heads, int rows, int64_t pages,
-                          int64_t head_stride, int64_t row_stride, int64_t page_stride, uint32_t box_rows);
+// Tensor map of rank `rank` (3 or 5) over bf16 data: dims and box innermost first, strides (in
+// elements) of dimensions 1 and up; 128-byte swizzle, out-of-bounds elements read as zero.
+bool make_tmap_bf16(CUtensorMap* map, const void* base, int rank, const int64_t* dims, const int64_t* strides,
+                    const int* box);
 
 // Streaming multiprocessors of the current device (cached).
 int sm_count();
