@@ -287,45 +287,44 @@ def gated_delta_rule(q, k, v, g, beta, o, h0=None, hT=None, scale=0.0, stream=No
 # A decoding step calls these for every layer, so each tensor is looked at once.
 
 
-def _dev() -> int:
-    """The current device, as the launch and its stream take it."""
-    return torch._C._cuda_getDevice()
+# The first line of each check is the whole of it for a good tensor; what is wrong is found after.
+_cuda_dev = torch._C._cuda_getDevice
+_cuda_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _raw_stream(stream, dev: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-
-
-def _at(t, name, dtype, dev, shape=None):
-    """Device pointer of a contiguous tensor of this dtype (and shape) on the current device."""
-    if t is None:
-        return None
+def _refuse(t, name, dtype, dev, shape):
     if t.get_device() != dev:
         raise ValueError(f"{name} is not on the current CUDA device")
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _rows_at(t, name, dtype, dev, shape, heads_apart=False):
-    """The same for a tensor whose last dimension alone has to be contiguous: (pointer, strides).
-    heads_apart: rows [N, H, d] whose heads follow one another."""
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is not on the current CUDA device")
-    if t.dtype != dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+def _at(t, name, dtype, dev, shape=None):
+    """Device pointer of a contiguous tensor of this dtype (and shape) on the current device."""
+    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and (shape is None or t.shape == shape):
+        return t.data_ptr()
+    _refuse(t, name, dtype, dev, shape)
+
+
+def _rows_at(t, name, dtype, dev, shape):
+    """Strides of a tensor whose last dimension alone has to be contiguous."""
     st = t.stride()
-    if st[-1] != 1 and shape[-1] > 1:
-        raise ValueError(f"the last dimension of {name} must be contiguous")
-    if heads_apart and st[1] != shape[2] and shape[1] > 1:
+    if t.dtype is dtype and t.get_device() == dev and t.shape == shape and st[-1] == 1:
+        return st
+    if t.shape == shape and shape[-1] == 1 and t.dtype == dtype and t.get_device() == dev:
+        return st
+    _refuse(t, f"the last dimension of {name}" if t.shape == shape else name, dtype, dev, shape)
+
+
+def _heads_at(t, name, dtype, dev, shape):
+    """Token stride of rows [N, H, d] whose heads follow one another."""
+    st = _rows_at(t, name, dtype, dev, shape)
+    if st[1] != shape[2] and shape[1] > 1:
         raise ValueError(f"the heads of {name} must be contiguous")
-    return t.data_ptr(), st
+    return st[0]
 
 
 def rope_table_scaled(method: str, theta: float, rd: int, max_len: int, factor: float = 1.0, orig_len: float = 0.0,
@@ -341,16 +340,16 @@ def rope_table_scaled(method: str, theta: float, rd: int, max_len: int, factor: 
 
 
 def _rope(fn, x, pos, rope_cs, out, layout, err_flag, stream):
-    dt, dev = _dt(x), _dev()
+    dt, dev, dtype = _dt(x), _cuda_dev(), x.dtype
     N, H, d = shape = x.shape
-    xp, xs = _rows_at(x, "x", x.dtype, dev, shape)
-    op, os = _rows_at(out, "out", x.dtype, dev, shape)
+    xs, os = _rows_at(x, "x", dtype, dev, shape), _rows_at(out, "out", dtype, dev, shape)
     max_len, half, two = rope_cs.shape
     if two != 2:
         raise ValueError("rope_cs must be [max_len, rd/2, 2]")
-    _call(fn, dt, xp, xs[0], xs[1], N, H, d, _at(pos, "pos", torch.int32, dev, (N,)),
-          _at(rope_cs, "rope_cs", torch.float32, dev), max_len, 2 * half, layout, op, os[0], os[1],
-          _at(err_flag, "err_flag", torch.int32, dev), _raw_stream(stream, dev))
+    _call(fn, dt, x.data_ptr(), xs[0], xs[1], N, H, d, _at(pos, "pos", torch.int32, dev, (N,)),
+          _at(rope_cs, "rope_cs", torch.float32, dev), max_len, 2 * half, layout, out.data_ptr(), os[0], os[1],
+          None if err_flag is None else _at(err_flag, "err_flag", torch.int32, dev),
+          _cuda_stream(dev) if stream is None else stream.cuda_stream)
 
 
 def rope(x, pos, rope_cs, out, layout=ROPE_HALF, err_flag=None, stream=None):
@@ -368,17 +367,17 @@ def rope_backward(dout, pos, rope_cs, dx, layout=ROPE_HALF, err_flag=None, strea
 def _cache(Kpages, Vpages, block_table, seq_len, q_off, Hkv, d, dtype, dev):
     """The batch and cache arguments both paged entry points take, checked: B, the pointer of
     q_off, K, V and the rest in the order of the C signature."""
-    P, page = Kpages.shape[:2]
-    shape = (P, page, Hkv, d)
-    kp, ks = _rows_at(Kpages, "Kpages", dtype, dev, shape)
-    vp, vs = _rows_at(Vpages, "Vpages", dtype, dev, shape)
-    if ks != vs:
+    shape = Kpages.shape
+    if shape[2:] != (Hkv, d):
+        raise ValueError(f"Kpages must be [num_pages, page, {Hkv}, {d}], not {tuple(shape)}")
+    ks = _rows_at(Kpages, "Kpages", dtype, dev, shape)
+    if _rows_at(Vpages, "Vpages", dtype, dev, shape) != ks:
         raise ValueError("Kpages and Vpages must have the same strides")
     B, = seq_len.shape
     max_pages = block_table.shape[-1]
-    return (B, _at(q_off, "q_off", torch.int64, dev, (B + 1,)), kp, vp, P, page, ks[0], ks[1], ks[2],
-            _at(block_table, "block_table", torch.int32, dev, (B, max_pages)), max_pages,
-            _at(seq_len, "seq_len", torch.int32, dev))
+    return (B, _at(q_off, "q_off", torch.int64, dev, (B + 1,)), Kpages.data_ptr(), Vpages.data_ptr(), shape[0],
+            shape[1], ks[0], ks[1], ks[2], _at(block_table, "block_table", torch.int32, dev, (B, max_pages)),
+            max_pages, _at(seq_len, "seq_len", torch.int32, dev))
 
 
 def paged_append(q, k, v, q_off, seq_len, block_table, Kpages, Vpages, rope_cs=None, q_out=None, pos=None,
@@ -386,26 +385,27 @@ def paged_append(q, k, v, q_off, seq_len, block_table, Kpages, Vpages, rope_cs=N
     """New tokens into the paged cache (msa_paged_append): k (rotated) and v [N, Hkv, d] into the
     pages [num_pages, page, Hkv, d] (any strides) of their sequences, q (rotated) into q_out.
     q may be None; rope_cs None: no rotation; pos None: cache positions."""
-    dt, dev, dtype = _dt(k), _dev(), k.dtype
-    N, Hkv, d = k.shape
-    kp, ks = _rows_at(k, "k", dtype, dev, (N, Hkv, d), True)
-    vp, vs = _rows_at(v, "v", dtype, dev, (N, Hkv, d), True)
-    if (q is None) != (q_out is None):
-        raise ValueError("q and q_out go together")
-    qp, qs, qop, qos, Hq = None, (0,), None, (0,), 0
-    if q is not None:
+    dt, dev, dtype = _dt(k), _cuda_dev(), k.dtype
+    N, Hkv, d = shape = k.shape
+    ks, vs = _heads_at(k, "k", dtype, dev, shape), _heads_at(v, "v", dtype, dev, shape)
+    qp = qop = csp = None
+    qs = qos = Hq = max_len = half = 0
+    if q is not None or q_out is not None:
+        if q is None or q_out is None:
+            raise ValueError("q and q_out go together")
         Hq = q.shape[1]
-        qp, qs = _rows_at(q, "q", dtype, dev, (N, Hq, d), True)
-        qop, qos = _rows_at(q_out, "q_out", dtype, dev, (N, Hq, d), True)
-    max_len = half = 0
+        qs, qos = _heads_at(q, "q", dtype, dev, (N, Hq, d)), _heads_at(q_out, "q_out", dtype, dev, (N, Hq, d))
+        qp, qop = q.data_ptr(), q_out.data_ptr()
     if rope_cs is not None:
         max_len, half, two = rope_cs.shape
         if two != 2:
             raise ValueError("rope_cs must be [max_len, rd/2, 2]")
+        csp = _at(rope_cs, "rope_cs", torch.float32, dev)
     B, qo, *cache = _cache(Kpages, Vpages, block_table, seq_len, q_off, Hkv, d, dtype, dev)
-    _call("msa_paged_append", dt, qp, qs[0], qop, qos[0], Hq, kp, ks[0], vp, vs[0], N, B, qo, Hkv, d,
-          _at(pos, "pos", torch.int32, dev, (N,)), _at(rope_cs, "rope_cs", torch.float32, dev), max_len, 2 * half,
-          layout, *cache, _at(err_flag, "err_flag", torch.int32, dev), _raw_stream(stream, dev))
+    _call("msa_paged_append", dt, qp, qs, qop, qos, Hq, k.data_ptr(), ks, v.data_ptr(), vs, N, B, qo, Hkv, d,
+          None if pos is None else _at(pos, "pos", torch.int32, dev, (N,)), csp, max_len, 2 * half, layout, *cache,
+          None if err_flag is None else _at(err_flag, "err_flag", torch.int32, dev),
+          _cuda_stream(dev) if stream is None else stream.cuda_stream)
 
 
 def paged_attn_workspace_size(dtype, B, max_q, Hq, Hkv, d, k=0, Mmax=0) -> int:
@@ -418,10 +418,10 @@ def paged_attn(Q, q_off, max_q, Kpages, Vpages, block_table, seq_len, O, ws, lse
     [N, Hq, d] packed by q_off int64 [B + 1] (at most max_q tokens a sequence), pages
     [num_pages, page, Hkv, d] (any strides), O [N, Hq, d], lse fp32 [Hq, N].  topk_idx int32 [B, k]
     with doc_chunk_off, Kbar and Vbar adds the selected documents' rows (at most Mmax)."""
-    dt, dev, dtype = _dt(Q), _dev(), Q.dtype
+    dt, dev, dtype = _dt(Q), _cuda_dev(), Q.dtype
     N, Hq, d = shape = Q.shape
     Hkv = Kpages.shape[2]
-    qp, qs = _rows_at(Q, "Q", dtype, dev, shape, True)
+    qs = _heads_at(Q, "Q", dtype, dev, shape)
     B, qo, *cache = _cache(Kpages, Vpages, block_table, seq_len, q_off, Hkv, d, dtype, dev)
     idx = off = kb = vb = None
     k = D = C = 0
@@ -432,8 +432,8 @@ def paged_attn(Q, q_off, max_q, Kpages, Vpages, block_table, seq_len, O, ws, lse
         idx = _at(topk_idx, "topk_idx", torch.int32, dev, (B, k))
         off = _at(doc_chunk_off, "doc_chunk_off", torch.int64, dev)
         kb, vb = _at(Kbar, "Kbar", dtype, dev, (C, Hkv, d)), _at(Vbar, "Vbar", dtype, dev, (C, Hkv, d))
-    if ws.get_device() != dev or not ws.is_contiguous():
-        raise ValueError("ws must be contiguous and on the current CUDA device")
-    _call("msa_paged_attn", dt, qp, qs[0], N, B, max_q, qo, Hq, Hkv, d, *cache, idx, k, off, D, C, kb, vb, Mmax, scale,
-          _at(O, "O", dtype, dev, shape), _at(lse, "lse", torch.float32, dev, (Hq, N)), ws.data_ptr(),
-          ws.numel() * ws.element_size(), _at(err_flag, "err_flag", torch.int32, dev), _raw_stream(stream, dev))
+    _call("msa_paged_attn", dt, Q.data_ptr(), qs, N, B, max_q, qo, Hq, Hkv, d, *cache, idx, k, off, D, C, kb, vb, Mmax,
+          scale, _at(O, "O", dtype, dev, shape),
+          None if lse is None else _at(lse, "lse", torch.float32, dev, (Hq, N)), _at(ws, "ws", ws.dtype, dev),
+          ws.nbytes, None if err_flag is None else _at(err_flag, "err_flag", torch.int32, dev),
+          _cuda_stream(dev) if stream is None else stream.cuda_stream)

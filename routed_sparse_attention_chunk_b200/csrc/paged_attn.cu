@@ -28,7 +28,7 @@ namespace {
 
 constexpr int kSub = 32;  // keys per step of the fp32 kernel
 constexpr int kF32Threads = 256;
-constexpr int kF32Slack = 2;  // tiles that not merging cut items is worth
+constexpr int kF32ItemCost = 1, kF32Slack = 2;  // see Split
 
 template <int DH, int RPT>
 struct F32Smem {
@@ -50,15 +50,16 @@ __global__ void __launch_bounds__(kF32Threads) paged_f32_kernel(PagedAttnArgs a,
   const PagedBatch& p = a.p;
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
   const int G = a.Hq / p.Hkv;
+  const Split sp{TB, kF32ItemCost, kF32Slack};
   pdl_wait();
-  find_start(p, TB, kF32Slack, blockIdx.x, gridDim.x, blockIdx.x == 0, &sm.st, reinterpret_cast<ScanScratch*>(sm.row));
-  if (tid == 0) leave_mark(&sm.st, TB, blockIdx.x, marks + blockIdx.x);
+  find_start(p, sp, blockIdx.x, gridDim.x, blockIdx.x == 0, &sm.st, reinterpret_cast<ScanScratch*>(sm.row));
+  if (tid == 0) leave_mark(&sm.st, sp, blockIdx.x, marks + blockIdx.x);
   pdl_trigger();
   if (!sm.st.any) return;
   const float sl2 = a.scale * 1.4426950408889634f;
   const float* Q = reinterpret_cast<const float*>(a.Q);
 
-  for (Walk w(TB, &sm.st); w.more(); w.next(p, TB)) {
+  for (Walk w(sp, &sm.st); w.more(); w.next(p, sp)) {
     const Seq& s = w.s;
     const int tb0 = w.i * TB;
     __syncthreads();  // the previous segment's readers are done
@@ -276,13 +277,16 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(MergeArgs a) {
   }
 }
 
+// CTAs of the fp32 kernel per SM, by its shared memory and registers.
+int f32_ctas(bool few) { return few ? 4 : 2; }
+
 template <int DH, int RPT>
 cudaError_t f32_t(const PagedAttnArgs& a, int TB, cudaStream_t s) {
   using S = F32Smem<DH, RPT>;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem(paged_f32_kernel<DH, RPT>, (int)sizeof(S), done);
   if (e != cudaSuccess) return e;
-  const int grid = 2 * sm_count();
+  const int grid = f32_ctas(RPT == 1) * sm_count();
   Mark* marks = reinterpret_cast<Mark*>(a.part);
   float* slots = reinterpret_cast<float*>(reinterpret_cast<char*>(a.part) + marks_bytes(grid));
   count_launch();
@@ -311,7 +315,7 @@ cudaError_t launch_merge(msa_dtype dt, int d, bool quads, const MergeArgs& a, in
 
 size_t paged_attn_partial_bytes(msa_dtype dt, int Hq, int Hkv, int d, int max_q) {
   const bool few = paged::few_rows(Hq, Hkv, max_q);
-  const int grid = dt == MSA_F32 ? 2 * sm_count() : sm_count();
+  const int grid = dt == MSA_F32 ? paged::f32_ctas(few) * sm_count() : sm_count();
   const int rows = dt == MSA_F32 ? (few ? 16 : 64) : (few && d == 128 ? Hq / Hkv * max_q : 128);
   return paged::marks_bytes(grid) + 2 * (size_t)grid * paged::slot_floats(rows, d) * sizeof(float);
 }

@@ -40,9 +40,9 @@ constexpr int kDH = 128;
 constexpr int kMaxRows = 16;            // R = G * Tq (the MMA's N, padded to 16)
 constexpr int kStages = 3;
 constexpr int kThreads = 192;
+constexpr int kItemCost = 2, kSlack = 0;  // see Split
 constexpr uint32_t kWaitPolls = 1u << 24;
 constexpr uint32_t kSpinLimit = 1u << 28;  // non-blocking polls of the MMA issuer without progress
-constexpr int kSlack = 4;  // tiles that not merging cut items is worth
 constexpr float kRescaleLog2 = 8.0f;
 
 struct DecParams {
@@ -126,7 +126,7 @@ paged_decode_kernel(const __grid_constant__ TileMaps maps, DecParams a) {
   Start* start = reinterpret_cast<Start*>(bars + 18);
 
   const PagedBatch& p = a.p;
-  const int TB = p.max_q;  // one block of tokens per sequence
+  const Split sp{p.max_q, kItemCost, kSlack};  // one block of tokens per sequence
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -148,8 +148,8 @@ paged_decode_kernel(const __grid_constant__ TileMaps maps, DecParams a) {
   }
   // a programmatic dependent: nothing an earlier kernel writes is read before this wait
   pdl_wait();
-  find_start(p, TB, kSlack, blockIdx.x, gridDim.x, blockIdx.x == 0, start, reinterpret_cast<ScanScratch*>(red_s));
-  if (tid == 0) leave_mark(start, TB, blockIdx.x, a.marks + blockIdx.x);
+  find_start(p, sp, blockIdx.x, gridDim.x, blockIdx.x == 0, start, reinterpret_cast<ScanScratch*>(red_s));
+  if (tid == 0) leave_mark(start, sp, blockIdx.x, a.marks + blockIdx.x);
   pdl_trigger();
   if (!start->any) return;
   if (warp == 1) {
@@ -172,7 +172,7 @@ paged_decode_kernel(const __grid_constant__ TileMaps maps, DecParams a) {
     auto locate = [&](const Walk& w, int t) {
       return locate_box(p, a.pm, a.seg_row, w.b, w.s.nm, w.s.len, t, lane);
     };
-    for (Walk w(TB, start); w.more() && !stop; w.next(p, TB)) {
+    for (Walk w(sp, start); w.more() && !stop; w.next(p, sp)) {
       Box x = locate(w, w.t0);
       for (int t = w.t0; t < w.t0 + w.n; ++t, ++it) {
         const uint32_t st = it % kStages;
@@ -214,7 +214,7 @@ paged_decode_kernel(const __grid_constant__ TileMaps maps, DecParams a) {
       constexpr uint32_t idO = idesc_bf16_f32(kDH, kMaxRows, /*b_mn=*/false, /*a_mn=*/true);  // V^T x P^T
       const uint32_t p0 = smem_u32(Ps);
       uint32_t it = 0, nseg = 0;  // it: tiles (K/V stages, S and P buffers); nseg: segments
-      for (Walk w(TB, start); w.more() && !*abort_s; w.next(p, TB), ++nseg) {
+      for (Walk w(sp, start); w.more() && !*abort_s; w.next(p, sp), ++nseg) {
         const int T = w.n;
         const uint32_t q0 = smem_u32(Qs + (nseg & 1) * DLayout::kQ);
         if (!mbar_wait_or_stop(q_ready, nseg & 1, kWaitPolls, abort_s)) break;
@@ -293,7 +293,7 @@ paged_decode_kernel(const __grid_constant__ TileMaps maps, DecParams a) {
         *reinterpret_cast<uint4*>(buf + sw128_off(r, c8, kMaxRows)) = v[k];
       }
     };
-    Walk w(TB, start);
+    Walk w(sp, start);
     {
       uint4 v[2];
       load_q(w, v);
@@ -313,7 +313,7 @@ paged_decode_kernel(const __grid_constant__ TileMaps maps, DecParams a) {
     while (w.more()) {
       // the next segment's Q rows, loaded now and stored after this segment's first tile
       Walk wn = w;
-      wn.next(p, TB);
+      wn.next(p, sp);
       const bool more = wn.more();
       uint4 qn[2];
       if (more) load_q(wn, qn);

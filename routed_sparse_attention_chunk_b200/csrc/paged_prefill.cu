@@ -48,8 +48,8 @@ using namespace paged;
 constexpr int kRows = 128;     // MMA M: query rows per block
 constexpr int kThreads = 384;  // K producer, S issuer, PV issuer, V producer, 2 x 4 softmax warps
 constexpr int kSoftRegs = 216, kOtherRegs = 72;  // 256 x 216 + 128 x 72 = 384 x 168, the launch's registers
+constexpr int kItemCost = 4, kSlack = 8;  // see Split
 constexpr uint32_t kWaitPolls = 1u << 24;
-constexpr int kSlack = 8;  // tiles that not merging cut items is worth
 constexpr float kRescaleLog2 = 8.0f;  // move the running max only when it grows by more than this
 
 struct PreParams {
@@ -152,6 +152,7 @@ paged_prefill_kernel(const __grid_constant__ TileMaps maps, PreParams a) {
 
   const PagedBatch& p = a.p;
   const int TB = a.TB;
+  const Split sp{TB, kItemCost, kSlack};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kKV; ++i) {
@@ -176,8 +177,8 @@ paged_prefill_kernel(const __grid_constant__ TileMaps maps, PreParams a) {
   }
   // a programmatic dependent: nothing an earlier kernel writes is read before this wait
   pdl_wait();
-  find_start(p, TB, kSlack, blockIdx.x, gridDim.x, blockIdx.x == 0, start, reinterpret_cast<ScanScratch*>(m_s));
-  if (threadIdx.x == 0) leave_mark(start, TB, blockIdx.x, a.marks + blockIdx.x);
+  find_start(p, sp, blockIdx.x, gridDim.x, blockIdx.x == 0, start, reinterpret_cast<ScanScratch*>(m_s));
+  if (threadIdx.x == 0) leave_mark(start, sp, blockIdx.x, a.marks + blockIdx.x);
   pdl_trigger();
   if (!start->any) return;
   if (warp == 1) {
@@ -210,7 +211,7 @@ paged_prefill_kernel(const __grid_constant__ TileMaps maps, PreParams a) {
       };
       uint32_t it = 0;
       bool stop = false;
-      for (Walk w(TB, start); w.more() && !stop; w.next(p, TB)) {
+      for (Walk w(sp, start); w.more() && !stop; w.next(p, sp)) {
         Box x = locate(w, w.t0);
         for (int t = w.t0; t < w.t0 + w.n; ++t, ++it) {
           const uint32_t st = it % kKV;
@@ -248,7 +249,7 @@ paged_prefill_kernel(const __grid_constant__ TileMaps maps, PreParams a) {
         const uint64_t dk0 = desc_k_sw128_sbo(smem_u32(Ks), Tile<DH>::kGroup);
         uint32_t g = 0, nseg = 0;
         bool ok = true;
-        for (Walk w(TB, start); ok && w.more(); w.next(p, TB), ++nseg) {
+        for (Walk w(sp, start); ok && w.more(); w.next(p, sp), ++nseg) {
           ok = wait(q_tmem, nseg & 1);
           for (int j = 0; ok && j < w.n; ++j, ++g) {
             const uint32_t ks = g % kKV;
@@ -277,7 +278,7 @@ paged_prefill_kernel(const __grid_constant__ TileMaps maps, PreParams a) {
         const uint64_t dv0 = desc_mn_sw128_sbo(smem_u32(Vs), 1024, Tile<DH>::kGroup);
         uint32_t g = 0, nseg = 0;
         bool ok = true;
-        for (Walk w(TB, start); ok && w.more(); w.next(p, TB), ++nseg) {
+        for (Walk w(sp, start); ok && w.more(); w.next(p, sp), ++nseg) {
           // the first PV of an item overwrites O once the last one has been read
           if (nseg > 0) ok = wait(o_read, (nseg - 1) & 1);
           for (int j = 0; ok && j < w.n; ++j, ++g) {
@@ -347,7 +348,7 @@ paged_prefill_kernel(const __grid_constant__ TileMaps maps, PreParams a) {
       mbar_arrive(q_tmem);
     };
     uint32_t g0 = 0, nseg = 0;  // tiles and items before this one
-    for (Walk w(TB, start); w.more(); w.next(p, TB), ++nseg) {
+    for (Walk w(sp, start); w.more(); w.next(p, sp), ++nseg) {
       const int t = w.i * TB + tl, n = w.n;
       const bool rvalid = tl < TB && t < w.s.nq;
       if (nseg == 0 && wg == 0) {
@@ -372,7 +373,7 @@ paged_prefill_kernel(const __grid_constant__ TileMaps maps, PreParams a) {
         if (next_q && j == j0) {
           // this item's S has begun, so its Q has left the shared memory
           Walk wn = w;
-          wn.next(p, TB);
+          wn.next(p, sp);
           fetch_q(row_of(wn));
         }
         if (next_q && j == n - 1) place_q();  // the item's last S is done: Q's columns are free

@@ -4,8 +4,9 @@
 // An item is one block of TB query tokens of one sequence for one KV head; its
 // keys are a list of 128-key tiles: the memory tiles of the sequence's segment
 // plan first, then the local tiles up to the block's last causal position.
-// All tiles of all items form one sequence f = 0 .. Ttot-1 (KV head outermost,
-// then sequence, block, tile), and CTA c takes the contiguous share
+// An item weighs its tiles plus `cost`, the tiles that its start and end take the
+// time of.  All items in a row (KV head outermost, then sequence, block) form one
+// sequence f = 0 .. Ttot-1 of such units, and CTA c takes the contiguous share
 // [c * per, (c + 1) * per), so every CTA streams the same number of tiles
 // whatever the lengths are; or, where there are no more items than CTAs and the
 // longest is at most `slack` tiles longer than that share, CTA c takes item c.  A stretch of the share inside one item is a
@@ -53,6 +54,9 @@ __device__ __forceinline__ Seq load_seq(const PagedBatch& p, int64_t b, int32_t*
   return s;
 }
 
+__device__ __forceinline__ int blocks_of(const Seq& s, int TB) {
+  return (int)(((uint32_t)s.nq + TB - 1) / (uint32_t)TB);
+}
 // Tiles of block i: the memory tiles and the local tiles up to the block's last
 // token's position; at least one, so that a block without a visible key is
 // still an item (its rows are written as zeros).
@@ -95,7 +99,7 @@ __device__ __forceinline__ int64_t sum_div_keys(uint32_t n, uint32_t a, uint32_t
 
 // Tiles of blocks [0, n) of a sequence.
 __device__ __forceinline__ int64_t tiles_before(const Seq& s, int TB, int n) {
-  const int nb = (int)(((uint32_t)s.nq + TB - 1) / (uint32_t)TB);
+  const int nb = blocks_of(s, TB);
   if (nb == 0 || n <= 0) return 0;
   const bool all = n >= nb;
   const int m = all ? nb - 1 : n;  // blocks of TB whole tokens
@@ -111,20 +115,21 @@ __device__ __forceinline__ int64_t tiles_before(const Seq& s, int TB, int n) {
   return all ? t + block_tiles(s, TB, nb - 1) : t;
 }
 
-// Largest item of a sequence: its last block (the only ones with more keys come later).
-__device__ __forceinline__ int largest_item(const Seq& s, int TB) {
-  const int nb = (int)(((uint32_t)s.nq + TB - 1) / (uint32_t)TB);
-  return nb ? block_tiles(s, TB, nb - 1) : 0;
-}
+// What a kernel's work looks like to the split.
+struct Split {
+  int TB;     // tokens of a block
+  int cost;   // an item's start and end, in tiles
+  int slack;  // tiles that not merging cut items is worth
+};
 
 struct Start {            // where a CTA's share begins
-  int64_t per, f0, f1;    // tiles per CTA, the share
-  int64_t b;              // sequence, KV head, block and tile of f0
+  int64_t per, f0, f1;    // units per CTA, the share
+  int64_t b;              // sequence, KV head, block of f0
   Seq s;
-  int g, i, t;
-  int any;                // the share is not empty
-  int one;                // the share is one whole item
-  int64_t rest;           // scratch: tile (or block) of the sequence
+  int g, i;
+  int o;                  // units of that item before f0
+  int any;                // the share has a tile
+  int64_t rest;           // scratch: unit (or block) of the sequence
 };
 
 struct ScanScratch {  // shared memory, free again after find_start
@@ -134,21 +139,23 @@ struct ScanScratch {  // shared memory, free again after find_start
 
 // All threads of the CTA call it (blockDim.x a multiple of 32, at most 512);
 // on return st (shared memory) holds share c of `grid` shares.
-__device__ __forceinline__ void find_start(const PagedBatch& p, int TB, int slack, int64_t c, int64_t grid,
+__device__ __forceinline__ void find_start(const PagedBatch& p, const Split& sp, int64_t c, int64_t grid,
                                            bool report, Start* st, ScanScratch* sc) {
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = nt >> 5;
+  const int TB = sp.TB;
   const int chunk = (int)(((uint32_t)p.B + nt - 1) / (uint32_t)nt);  // B < 2^31
   const int64_t b0 = min(p.B, (int64_t)tid * chunk), b1 = min(p.B, b0 + chunk);
-  int64_t mine = 0;   // tiles of this thread's sequences
-  int items = 0, most = 0;  // their blocks (at most N < 2^31), the largest of them
+  int64_t mine = 0;         // units of this thread's sequences
+  int items = 0, most = 0;  // their blocks (at most N < 2^31), the tiles of the largest
   Seq s;
   for (int64_t b = b0; b < b1; ++b) {
     s = load_seq(p, b, report ? p.err_flag : nullptr);
-    mine += tiles_before(s, TB, 0x7fffffff);
-    items += (int)(((uint32_t)s.nq + TB - 1) / (uint32_t)TB);
-    most = max(most, largest_item(s, TB));
+    const int nb = blocks_of(s, TB);
+    mine += tiles_before(s, TB, nb) + (int64_t)nb * sp.cost;
+    items += nb;
+    if (nb > 0) most = max(most, block_tiles(s, TB, nb - 1));  // no block has more keys than the last
   }
-  // only the first warps have sequences when there are few: the others' sums are 0
+  // the warps past the last sequence take no part in the scan
   const int used = (int)min((int64_t)warps, (p.B + 31 * (int64_t)chunk) / (32 * (int64_t)chunk) + 1);
   int64_t incl = mine;
   int icl = items;
@@ -189,20 +196,20 @@ __device__ __forceinline__ void find_start(const PagedBatch& p, int TB, int slac
   const bool small = Ttot + grid < 0x7fffffff;
   const int64_t per = max((int64_t)1, small ? (int64_t)((uint32_t)(Ttot + grid - 1) / (uint32_t)grid)
                                             : (Ttot + grid - 1) / grid);
-  const bool one = (int64_t)n_items * p.Hkv <= grid && most <= per + slack;  // an item per CTA
+  // an item per CTA, if there are no more and none is too long
+  const bool one = (int64_t)n_items * p.Hkv <= grid && most + sp.cost <= per + sp.slack;
   const int64_t f0 = c * per;
   const bool any = one ? c < (int64_t)n_items * p.Hkv : f0 < Ttot;
-  // KV head, and the tile (or block) of that head where the share begins
+  // KV head, and the unit (or block) of that head where the share begins
   const int64_t div = one ? n_items : total, at = one ? c : f0;
   const int64_t g = !any ? 0 : small ? (int64_t)((uint32_t)at / (uint32_t)div) : at / div;
   const int64_t w = at - g * div;
   if (tid == 0) {
     st->per = per;
     st->f0 = one ? 0 : f0;
-    if (!one) st->f1 = min(f0 + per, Ttot);
-    st->any = any;
-    st->one = one;
+    st->f1 = min(f0 + per, Ttot);
     st->g = (int)g;
+    if (!any) st->any = 0;
   }
   const int64_t lo_w = one ? icl - items : incl - mine, hi_w = one ? icl : incl;
   if (any && w >= lo_w && w < hi_w) {  // exactly one thread
@@ -210,7 +217,8 @@ __device__ __forceinline__ void find_start(const PagedBatch& p, int TB, int slac
     if (chunk > 1) {
       for (;;) {
         s = load_seq(p, b);
-        const int64_t n = one ? (int64_t)(((uint32_t)s.nq + TB - 1) / (uint32_t)TB) : tiles_before(s, TB, 0x7fffffff);
+        const int nb = blocks_of(s, TB);
+        const int64_t n = one ? nb : tiles_before(s, TB, nb) + (int64_t)nb * sp.cost;
         if (rest < n) break;
         rest -= n;
         ++b;
@@ -219,57 +227,61 @@ __device__ __forceinline__ void find_start(const PagedBatch& p, int TB, int slac
     st->b = b;
     st->s = s;
     st->rest = rest;
-    if (one) {
-      st->i = (int)rest;
-      st->t = 0;
-      st->f1 = block_tiles(s, TB, (int)rest);
-    }
   }
   __syncthreads();
-  if (any && !one) {
-    if (warp == 0) {
-      // the block holding tile `rest`: the last one with tiles_before(block) <= rest, 32 probes at a time
-      const Seq q = st->s;
-      const int64_t rest = st->rest;
-      int lo = 0, n = (int)(((uint32_t)q.nq + TB - 1) / (uint32_t)TB);  // answer in [lo, lo + n)
+  if (any && warp == 0) {
+    const Seq q = st->s;
+    const int64_t rest = st->rest;
+    int lo = one ? (int)rest : 0;
+    if (!one) {
+      // the block holding unit `rest`: the last one with no more units before it, 32 probes at a time
+      int n = blocks_of(q, TB);  // answer in [lo, lo + n)
       while (n > 1) {
         const int step = (n + 31) >> 5;
         const int probe = lo + lane * step;
-        const unsigned hit = __ballot_sync(0xffffffffu, lane * step < n && tiles_before(q, TB, probe) <= rest);
+        const unsigned hit = __ballot_sync(
+            0xffffffffu, lane * step < n && tiles_before(q, TB, probe) + (int64_t)probe * sp.cost <= rest);
         const int last = 31 - __clz(hit);  // lane 0 always hits
         lo += last * step;
         n = min(step, n - last * step);
       }
-      if (lane == 0) {
-        st->i = lo;
-        st->t = (int)(rest - tiles_before(q, TB, lo));
-      }
     }
-    __syncthreads();
+    if (lane == 0) {
+      const int o = one ? 0 : (int)(rest - tiles_before(q, TB, lo) - (int64_t)lo * sp.cost);
+      const int T = block_tiles(q, TB, lo);
+      if (one) st->f1 = sp.cost + T;
+      st->i = lo;
+      st->o = o;
+      // a share may hold nothing but the start of an item that the next one takes
+      st->any = min((int64_t)T, o + (st->f1 - st->f0) - sp.cost) > max(0, o - sp.cost);
+    }
   }
+  __syncthreads();
 }
 
-// Walks a CTA's share segment by segment.
+// Walks a CTA's share segment by segment (only if the share has a tile).
 struct Walk {
   int64_t f, f1, b;
-  int g, i, t0, T, n;  // item, first tile of the segment, tiles of the item, tiles of the segment
+  int g, i, o, t0, T, n;  // item, units of it before f, first tile of the segment, tiles of item and segment
   Seq s;
-  __device__ __forceinline__ void span(int TB) {
-    T = block_tiles(s, TB, i);
-    n = (int)min((int64_t)(T - t0), f1 - f);
+  __device__ __forceinline__ void span(const Split& sp) {
+    T = block_tiles(s, sp.TB, i);
+    t0 = max(0, o - sp.cost);
+    n = (int)min((int64_t)T, f1 - f + o - sp.cost) - t0;
+    if (n <= 0) f = f1;  // the share ends before the item's first tile
   }
-  __device__ __forceinline__ Walk(int TB, const Start* st)
-      : f(st->f0), f1(st->f1), b(st->b), g(st->g), i(st->i), t0(st->t), s(st->s) {
-    span(TB);
+  __device__ __forceinline__ Walk(const Split& sp, const Start* st)
+      : f(st->f0), f1(st->f1), b(st->b), g(st->g), i(st->i), o(st->o), s(st->s) {
+    span(sp);
   }
   __device__ __forceinline__ bool more() const { return f < f1; }
   __device__ __forceinline__ bool whole() const { return n == T; }
   // Call only while more(); afterwards the item fields hold the next segment if more().
-  __device__ __forceinline__ void next(const PagedBatch& p, int TB) {
-    f += n;
+  __device__ __forceinline__ void next(const PagedBatch& p, const Split& sp) {
+    f += sp.cost + T - o;
     if (f >= f1) return;
-    t0 = 0;
-    if ((int64_t)++i * TB >= s.nq) {
+    o = 0;
+    if ((int64_t)++i * sp.TB >= s.nq) {
       i = 0;
       do {
         if (++b == p.B) {
@@ -279,7 +291,7 @@ struct Walk {
         s = load_seq(p, b);
       } while (s.nq == 0);
     }
-    span(TB);
+    span(sp);
   }
 };
 
@@ -293,16 +305,17 @@ struct Mark {
   int32_t tokens;  // of the item
   int32_t g;       // KV head
 };
-__device__ __forceinline__ void leave_mark(const Start* st, int TB, int64_t c, Mark* m) {
+__device__ __forceinline__ void leave_mark(const Start* st, const Split& sp, int64_t c, Mark* m) {
   Mark v = {};
-  if (st->any && st->t > 0 && st->t <= st->per) {  // not cut at an earlier border already
-    const int64_t start = st->f0 - st->t, end = start + block_tiles(st->s, TB, st->i);
-    v.row = st->s.q0 + (int64_t)st->i * TB;
+  const int t = st->o - sp.cost;  // tiles of the item before the border
+  if (st->any && t > 0 && t <= st->per) {  // not cut at an earlier border already
+    const int64_t end = st->f0 - t + block_tiles(st->s, sp.TB, st->i);
+    v.row = st->s.q0 + (int64_t)st->i * sp.TB;
     v.c0 = c - 1;
-    v.late = st->t != st->per;
+    v.late = st->o < st->per;
     v.n = 2;
     for (int64_t at = st->f1; at < end; at += st->per) ++v.n;
-    v.tokens = min(TB, st->s.nq - st->i * TB);
+    v.tokens = min(sp.TB, st->s.nq - st->i * sp.TB);
     v.g = st->g;
   }
   *m = v;
