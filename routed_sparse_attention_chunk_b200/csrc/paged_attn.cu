@@ -215,6 +215,7 @@ __global__ void __launch_bounds__(kF32Threads) paged_f32_kernel(PagedAttnArgs a,
 // takes kMergeRows of its rows, a thread four values of a row.  A chain of dependent
 // loads (mark, maxima, values) bounds it; all blocks are resident at once.
 constexpr int kMergeThreads = 256, kMergeRows = 32;
+constexpr int kAtOnce = 8;  // segments whose loads are in flight together
 template <typename T, int DH, bool kQuads>
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(MergeArgs a) {
   constexpr int kPairs = kMergeRows * (DH / 4);  // (row, four values) pairs of the block
@@ -224,7 +225,6 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(MergeArgs a) {
   const size_t sf = slot_floats(a.rows, DH);
   const float* first = a.slots + (2 * mk.c0 + mk.late) * sf;
   const float* rest = a.slots + 2 * mk.c0 * sf;  // segment x > 0 is in slot 2 (c0 + x)
-#pragma unroll 2
   for (int e = threadIdx.x; e < kPairs; e += kMergeThreads) {
     // consecutive threads: rows first in the quads layout, values of a row first in the other
     const int quad = kQuads ? e / kMergeRows : e % (DH / 4);
@@ -232,26 +232,26 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(MergeArgs a) {
     if (r >= last) continue;
     const int ml_at = a.rows * DH + 2 * r, v_at = kQuads ? (quad * a.rows + r) * 4 : r * DH + quad * 4;
     float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int x0 = 0; x0 < mk.n; x0 += 4) {
-      float2 ml[4];
-      float4 v[4];
+    for (int x0 = 0; x0 < mk.n; x0 += kAtOnce) {
+      float2 ml[kAtOnce];
+      float4 v[kAtOnce];
       float top = m;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < kAtOnce; ++j) {
         if (x0 + j >= mk.n) continue;
         const float* src = x0 + j == 0 ? first : rest + 2 * (size_t)(x0 + j) * sf;
         ml[j] = *reinterpret_cast<const float2*>(src + ml_at);
         v[j] = *reinterpret_cast<const float4*>(src + v_at);
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < kAtOnce; ++j)
         if (x0 + j < mk.n) top = fmaxf(top, ml[j].x);
       const float corr = l == 0.f ? 0.f : exp2f((m - top) * a.unit_log2);
       l *= corr;
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[i] *= corr;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < kAtOnce; ++j) {
         if (x0 + j >= mk.n) continue;
         const float w = ml[j].y == 0.f ? 0.f : exp2f((ml[j].x - top) * a.unit_log2);  // sum 0: no key was visible
         l += w * ml[j].y;

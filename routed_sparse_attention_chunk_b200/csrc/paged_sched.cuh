@@ -137,12 +137,103 @@ struct ScanScratch {  // shared memory, free again after find_start
   int counts[16], tops[16];
 };
 
+// The block of sequence q that holds unit `rest`: the last one with no more units before it, 32
+// probes at a time.  A whole warp calls it; every lane gets the answer.
+__device__ __forceinline__ int find_block(const Seq& q, const Split& sp, int64_t rest, int lane) {
+  int lo = 0, n = blocks_of(q, sp.TB);  // answer in [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 31) >> 5;
+    const int probe = lo + lane * step;
+    const unsigned hit = __ballot_sync(
+        0xffffffffu, lane * step < n && tiles_before(q, sp.TB, probe) + (int64_t)probe * sp.cost <= rest);
+    const int last = 31 - __clz(hit);  // lane 0 always hits
+    lo += last * step;
+    n = min(step, n - last * step);
+  }
+  return lo;
+}
+
+// Where the share begins inside item (g, b, block i): the last part of find_start, by one thread.
+__device__ __forceinline__ void set_start(const Split& sp, int64_t rest, bool one, const Seq& q, int lo, Start* st) {
+  const int o = one ? 0 : (int)(rest - tiles_before(q, sp.TB, lo) - (int64_t)lo * sp.cost);
+  const int T = block_tiles(q, sp.TB, lo);
+  if (one) st->f1 = sp.cost + T;
+  st->i = lo;
+  st->o = o;
+  // a share may hold nothing but the start of an item that the next one takes
+  st->any = min((int64_t)T, o + (st->f1 - st->f0) - sp.cost) > max(0, o - sp.cost);
+}
+
+// find_start for at most 32 sequences whose units all together stay below 2^31: one warp, a
+// sequence per lane, in 32 bits.  False (in every lane) if they do not fit.  A kernel over a short
+// cache spends a good part of its time before its first load (2.3 of 7 us in the general form).
+__device__ __forceinline__ bool find_start_small(const PagedBatch& p, const Split& sp, int64_t c, int64_t grid,
+                                                 bool report, int lane, Start* st) {
+  Seq s{0, 0, 0, 0};
+  if (lane < p.B) s = load_seq(p, lane, report ? p.err_flag : nullptr);
+  const int nb = blocks_of(s, sp.TB);
+  const int last = nb > 0 ? block_tiles(s, sp.TB, nb - 1) : 0;
+  // no block has more keys than the last one
+  if (__any_sync(0xffffffffu, (int64_t)nb * (last + sp.cost) * p.Hkv >= (1 << 25))) return false;
+  const int mine = nb > 0 ? (int)tiles_before(s, sp.TB, nb - 1) + last + nb * sp.cost : 0;
+  int incl = mine, icl = nb;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o), u = __shfl_up_sync(0xffffffffu, icl, o);
+    if (lane >= o) {
+      incl += v;
+      icl += u;
+    }
+  }
+  const int total = __shfl_sync(0xffffffffu, incl, 31), items = __shfl_sync(0xffffffffu, icl, 31);
+  const int most = __reduce_max_sync(0xffffffffu, last);
+  const int Ttot = total * p.Hkv;
+  const int per = max(1, (int)((uint32_t)(Ttot + (int)grid - 1) / (uint32_t)grid));
+  const bool one = items * p.Hkv <= grid && most + sp.cost <= per + sp.slack;
+  const int64_t f0 = c * per;
+  const bool any = one ? c < items * p.Hkv : f0 < Ttot;
+  if (!any) {
+    if (lane == 0) st->any = 0;
+    return true;
+  }
+  const uint32_t div = one ? items : total, at = one ? (uint32_t)c : (uint32_t)f0;
+  const int g = (int)(at / div), w = (int)(at - g * div);
+  const int lo_w = one ? icl - nb : incl - mine, hi_w = one ? icl : incl;
+  const int b = __ffs(__ballot_sync(0xffffffffu, w >= lo_w && w < hi_w)) - 1;
+  Seq q;
+  q.q0 = __shfl_sync(0xffffffffu, s.q0, b);
+  q.nq = __shfl_sync(0xffffffffu, s.nq, b);
+  q.len = __shfl_sync(0xffffffffu, s.len, b);
+  q.nm = __shfl_sync(0xffffffffu, s.nm, b);
+  const int rest = w - __shfl_sync(0xffffffffu, lo_w, b);
+  const int lo = one ? rest : find_block(q, sp, rest, lane);
+  if (lane == 0) {
+    st->per = per;
+    st->f0 = one ? 0 : f0;
+    st->f1 = min(f0 + per, (int64_t)Ttot);
+    st->g = g;
+    st->b = b;
+    st->s = q;
+    set_start(sp, rest, one, q, lo, st);
+  }
+  return true;
+}
+
 // All threads of the CTA call it (blockDim.x a multiple of 32, at most 512);
 // on return st (shared memory) holds share c of `grid` shares.
 __device__ __forceinline__ void find_start(const PagedBatch& p, const Split& sp, int64_t c, int64_t grid,
                                            bool report, Start* st, ScanScratch* sc) {
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = nt >> 5;
   const int TB = sp.TB;
+  if (p.B <= 32) {
+    if (warp == 0) {
+      const bool done = find_start_small(p, sp, c, grid, report, lane, st);
+      if (lane == 0) sc->counts[0] = done;
+    }
+    __syncthreads();
+    if (sc->counts[0]) return;
+    __syncthreads();  // the scratch is written again
+  }
   const int chunk = (int)(((uint32_t)p.B + nt - 1) / (uint32_t)nt);  // B < 2^31
   const int64_t b0 = min(p.B, (int64_t)tid * chunk), b1 = min(p.B, b0 + chunk);
   int64_t mine = 0;         // units of this thread's sequences
@@ -232,29 +323,8 @@ __device__ __forceinline__ void find_start(const PagedBatch& p, const Split& sp,
   if (any && warp == 0) {
     const Seq q = st->s;
     const int64_t rest = st->rest;
-    int lo = one ? (int)rest : 0;
-    if (!one) {
-      // the block holding unit `rest`: the last one with no more units before it, 32 probes at a time
-      int n = blocks_of(q, TB);  // answer in [lo, lo + n)
-      while (n > 1) {
-        const int step = (n + 31) >> 5;
-        const int probe = lo + lane * step;
-        const unsigned hit = __ballot_sync(
-            0xffffffffu, lane * step < n && tiles_before(q, TB, probe) + (int64_t)probe * sp.cost <= rest);
-        const int last = 31 - __clz(hit);  // lane 0 always hits
-        lo += last * step;
-        n = min(step, n - last * step);
-      }
-    }
-    if (lane == 0) {
-      const int o = one ? 0 : (int)(rest - tiles_before(q, TB, lo) - (int64_t)lo * sp.cost);
-      const int T = block_tiles(q, TB, lo);
-      if (one) st->f1 = sp.cost + T;
-      st->i = lo;
-      st->o = o;
-      // a share may hold nothing but the start of an item that the next one takes
-      st->any = min((int64_t)T, o + (st->f1 - st->f0) - sp.cost) > max(0, o - sp.cost);
-    }
+    const int lo = one ? (int)rest : find_block(q, sp, rest, lane);
+    if (lane == 0) set_start(sp, rest, one, q, lo, st);
   }
   __syncthreads();
 }
