@@ -5,7 +5,7 @@
 // position (the cache position unless one is given).
 //
 // Bound by memory: q, k and v are read once, q_out and the cache rows written
-// once.  A thread takes one unit (two 16-byte vectors) of up to four of the
+// once.  A thread takes one unit (two 16-byte vectors) of two of the
 // token's heads (queries, keys, values in that order): their loads go out first,
 // and the token's place (its sequence, its block-table entry, the table's pairs: a
 // chain of dependent loads) is found while they are in flight.
@@ -17,7 +17,7 @@ namespace msa {
 namespace {
 
 template <typename T, bool kInter>
-__global__ void __launch_bounds__(256) paged_append_kernel(PagedAppendArgs a, int units, int groups, int64_t total) {
+__global__ void __launch_bounds__(kRopeThreads) paged_append_kernel(PagedAppendArgs a, int units, int groups, int64_t total) {
   pdl_wait();  // the offsets, lengths and projections may come from the previous kernel
   const PagedBatch& p = a.p;
   const int Hkv = p.Hkv, Hq = a.q ? a.Hq : 0, heads = Hq + 2 * Hkv;
@@ -40,8 +40,8 @@ __global__ void __launch_bounds__(256) paged_append_kernel(PagedAppendArgs a, in
       else if (h < Hq + Hkv) src = reinterpret_cast<const T*>(a.k) + n * a.k_ts + (h - Hq) * a.d;
       else src = reinterpret_cast<const T*>(a.v) + n * a.v_ts + (h - Hq - Hkv) * a.d;
       const bool val = h >= Hq + Hkv;
-      v0[j] = *reinterpret_cast<const uint4*>(src + (val ? at1v - Vec<T>::N : rot.at0));
-      v1[j] = *reinterpret_cast<const uint4*>(src + (val ? at1v : rot.at1));
+      v0[j] = load_stream(src + (val ? at1v - Vec<T>::N : rot.at0));
+      v1[j] = load_stream(src + (val ? at1v : rot.at1));
     }
   }
   // the last sequence whose offset is at or before n; the proportional guess is right for one
@@ -85,8 +85,8 @@ __global__ void __launch_bounds__(256) paged_append_kernel(PagedAppendArgs a, in
       else if (!val) dst = reinterpret_cast<T*>(a.K) + base + (h - Hq) * a.head_stride;
       else dst = reinterpret_cast<T*>(a.V) + base + (h - Hq - Hkv) * a.head_stride;
       if (rot.rotated && !val) turn.apply(v0[j], v1[j], kInter);
-      *reinterpret_cast<uint4*>(dst + (val ? at1v - Vec<T>::N : rot.at0)) = v0[j];
-      *reinterpret_cast<uint4*>(dst + (val ? at1v : rot.at1)) = v1[j];
+      store_stream(dst + (val ? at1v - Vec<T>::N : rot.at0), v0[j]);
+      store_stream(dst + (val ? at1v : rot.at1), v1[j]);
     }
   }
 }
@@ -96,11 +96,11 @@ cudaError_t append_t(const PagedAppendArgs& a, cudaStream_t s) {
   const int units = RopeUnit<T>::per_head(a.d);
   const int groups = ((a.q ? a.Hq : 0) + 2 * a.p.Hkv + kRopeHeads - 1) / kRopeHeads;
   const int64_t total = a.p.N * units * groups;
-  const int64_t blocks = (total + 255) / 256;
+  const int64_t blocks = (total + kRopeThreads - 1) / kRopeThreads;
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;  // grid x
   count_launch();
   return launch_pdl(a.interleaved ? paged_append_kernel<T, true> : paged_append_kernel<T, false>,
-                    dim3((unsigned)blocks), dim3(256), 0, s, a, units, groups, total);
+                    dim3((unsigned)blocks), dim3(kRopeThreads), 0, s, a, units, groups, total);
 }
 
 }  // namespace

@@ -6,8 +6,8 @@
 // in fp32, rounded once on the store; the dimensions past rd are copied.
 //
 // Bound by memory (3 flop per 8 bytes): every vector of x is read and written
-// once.  A thread takes one unit (two vectors) of up to four heads of a token, so
-// the table's pairs are read once for them and eight loads are in flight.
+// once.  A thread takes one unit (two vectors) of two heads of a token, so the
+// table's pairs are read once for both and four loads are in flight.
 #include "common.cuh"
 #include "internal.h"
 #include "rope.cuh"
@@ -18,7 +18,7 @@ namespace {
 // A programmatic dependent: it may start while the previous kernel of the stream
 // drains, and reads nothing that kernel writes before the wait.
 template <typename T, bool kInter>
-__global__ void __launch_bounds__(256) rope_kernel(RopeArgs a, int units, int groups, int64_t total) {
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs a, int units, int groups, int64_t total) {
   pdl_wait();
   const int64_t id = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (id >= total) return;
@@ -35,8 +35,8 @@ __global__ void __launch_bounds__(256) rope_kernel(RopeArgs a, int units, int gr
     const int h = (int)hg + j * groups;
     if (h < a.H) {
       const T* src = x + h * a.x_hs;
-      p[j] = *reinterpret_cast<const uint4*>(src + unit.at0);
-      q[j] = *reinterpret_cast<const uint4*>(src + unit.at1);
+      p[j] = load_stream(src + unit.at0);
+      q[j] = load_stream(src + unit.at1);
     }
   }
   if (pos < 0 || pos >= a.max_len) {
@@ -51,8 +51,8 @@ __global__ void __launch_bounds__(256) rope_kernel(RopeArgs a, int units, int gr
     if (h < a.H) {
       if (unit.rotated) turn.apply(p[j], q[j], kInter);
       T* dst = y + h * a.out_hs;
-      *reinterpret_cast<uint4*>(dst + unit.at0) = p[j];
-      *reinterpret_cast<uint4*>(dst + unit.at1) = q[j];
+      store_stream(dst + unit.at0, p[j]);
+      store_stream(dst + unit.at1, q[j]);
     }
   }
 }
@@ -61,10 +61,10 @@ template <typename T>
 cudaError_t rope_t(const RopeArgs& a, cudaStream_t s) {
   const int units = RopeUnit<T>::per_head(a.d), groups = (a.H + kRopeHeads - 1) / kRopeHeads;
   const int64_t total = a.N * units * groups;
-  const int64_t blocks = (total + 255) / 256;
+  const int64_t blocks = (total + kRopeThreads - 1) / kRopeThreads;
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;  // grid x
   count_launch();
-  return launch_pdl(a.interleaved ? rope_kernel<T, true> : rope_kernel<T, false>, dim3((unsigned)blocks), dim3(256), 0,
+  return launch_pdl(a.interleaved ? rope_kernel<T, true> : rope_kernel<T, false>, dim3((unsigned)blocks), dim3(kRopeThreads), 0,
                     s, a, units, groups, total);
 }
 
