@@ -633,8 +633,9 @@ msa_status msa_paged_append(msa_dtype dt, const void* q, int64_t q_tok_stride, v
  *   O        [N, Hq, d] dtype dt, dense;  lse fp32 [Hq, N] or NULL
  *   scale    <= 0 means 1/sqrt(d)
  * A token that sees no key (a position before 0, no memory rows) gets O = 0 and
- * lse = -inf.  Cached rows at positions the sequence has (below seq_len) and bank
- * rows must hold finite values; every other row of a page may hold anything.
+ * lse = -inf.  A key that a token does not see never reaches its output, whatever
+ * its K and V rows hold (NaN and infinities included): later tokens, the rest of
+ * a sequence's last page, the bank rows beside a selected run.
  * Supported: Hq % Hkv == 0, at most 64 query heads per KV head.  bf16 runs on the
  * tensor cores, fp32 in fp32.  The result does not depend on timing: partial sums
  * are merged in a fixed order.

@@ -216,21 +216,109 @@ __global__ void __launch_bounds__(kF32Threads) paged_f32_kernel(PagedAttnArgs a,
 // loads (mark, maxima, values) bounds it; all blocks are resident at once.
 constexpr int kMergeThreads = 256, kMergeRows = 32;
 constexpr int kAtOnce = 8;  // segments whose loads are in flight together
+
+// The whole batch on the CUDA cores, for bf16 batches with values that are not finite among keys
+// that only some rows see.  Half a warp takes one (token, head) row at a time, a lane DH / 16 of
+// its dimensions, and goes through the keys the row sees with a running maximum and sum.  A key
+// that it does not see is never read; one that it sees keeps a weight above 0, so that an infinity
+// stays one.  Slow, and without shared memory: the merging blocks sit beside the kernel they wait for.
+template <int DH>
+__device__ __forceinline__ void attend_all(const PagedAttnArgs& a) {
+  constexpr int DPT = DH / 16;  // 4 or 8 bf16 values: 8 or 16 bytes
+  const PagedBatch& p = a.p;
+  const int G = a.Hq / p.Hkv, x0 = (threadIdx.x & 15) * DPT;
+  const float sl2 = a.scale * 1.4426950408889634f;
+  const int64_t me = ((int64_t)blockIdx.x + (int64_t)blockIdx.y * gridDim.x) * (kMergeThreads / 16) + (threadIdx.x >> 4);
+  const int64_t all = (int64_t)gridDim.x * gridDim.y * (kMergeThreads / 16);
+  auto load = [&](const void* base, int64_t off, float (&f)[DPT]) {
+    const __nv_bfloat162* src = reinterpret_cast<const __nv_bfloat162*>(reinterpret_cast<const __nv_bfloat16*>(base) + off + x0);
+#pragma unroll
+    for (int i = 0; i < DPT / 2; ++i) {
+      const float2 v = __bfloat1622float2(src[i]);
+      f[2 * i] = v.x;
+      f[2 * i + 1] = v.y;
+    }
+  };
+  for (int64_t b = 0; b < p.B; ++b) {
+    const Seq s = load_seq(p, b);
+    const int64_t rows = (int64_t)s.nq * a.Hq;
+    // the two halves of a warp step together: rows past the last are computed again, not written
+    for (int64_t x = me; (x & ~int64_t(1)) < rows; x += all) {
+      const int64_t r = min(x, rows - 1);
+      const int t = (int)(r / a.Hq), h = (int)(r - (int64_t)t * a.Hq), g = h / G;
+      const int local = max(0, s.len - s.nq + t + 1), mem = s.nm * kKeys;
+      float q[DPT], o[DPT], m = -INFINITY, l = 0.f;
+      load(a.Q, (s.q0 + t) * a.q_ts + h * DH, q);
+#pragma unroll
+      for (int i = 0; i < DPT; ++i) o[i] = 0.f;
+      const int keys = mem + local, most = max(keys, __shfl_xor_sync(0xffffffffu, keys, 16));
+      for (int k = 0; k < most; ++k) {
+        bool sees = k < keys;
+        const void *kb = a.K, *vb = a.V;
+        int64_t off = -1;
+        if (k < mem) {
+          const int sg = k / kSegRows;
+          sees = sg < p.Smax && k % kSegRows < __ldg(a.seg_cnt + b * p.Smax + sg);
+          if (sees) off = ((int64_t)(__ldg(a.seg_row + b * p.Smax + sg) + k % kSegRows) * p.Hkv + g) * DH;
+          kb = a.Kbar;
+          vb = a.Vbar;
+        } else if (sees) {
+          const int at = k - mem, pi = at / p.page;
+          const int64_t pg = __ldg(p.table + b * p.max_pages + pi);
+          if (pg >= 0 && pg < p.num_pages) off = pg * a.page_stride + (at - pi * p.page) * a.row_stride + g * a.head_stride;
+        }
+        float kf[DPT] = {}, vf[DPT] = {}, dot = 0.f;
+        if (off >= 0) {
+          load(kb, off, kf);
+          load(vb, off, vf);
+        }
+#pragma unroll
+        for (int i = 0; i < DPT; ++i) dot = fmaf(q[i], kf[i], dot);
+#pragma unroll
+        for (int y = 8; y > 0; y >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, y);
+        if (!sees) continue;
+        const float m_new = fmaxf(m, dot);
+        const float corr = m == -INFINITY ? 0.f : exp2f((m - m_new) * sl2), e = exp2f((dot - m_new) * sl2);
+        const float w = e < 1.17549435e-38f ? 1.17549435e-38f : e;  // (a NaN stays)
+        l = l * corr + w;
+        m = m_new;
+#pragma unroll
+        for (int i = 0; i < DPT; ++i) o[i] = fmaf(w, vf[i], corr == 0.f ? 0.f : o[i] * corr);
+      }
+      if (x >= rows) continue;
+      const int64_t out = s.q0 + t;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(a.O) + (out * a.Hq + h) * DH + x0;
+#pragma unroll
+      for (int i = 0; i < DPT; ++i) dst[i] = __float2bfloat16_rn(l == 0.f ? 0.f : o[i] * inv);
+      if (a.lse && x0 == 0) a.lse[(int64_t)h * p.N + out] = l == 0.f ? -INFINITY : m * a.scale + logf(l);
+    }
+  }
+}
+
 template <typename T, int DH, bool kQuads>
-__global__ void __launch_bounds__(kMergeThreads) merge_kernel(MergeArgs a) {
+__global__ void __launch_bounds__(kMergeThreads, 4) merge_kernel(MergeArgs ma) {
   constexpr int kPairs = kMergeRows * (DH / 4);  // (row, four values) pairs of the block
   pdl_wait();
-  const Mark mk = a.marks[blockIdx.x + 1];
-  const int last = mk.tokens * a.G;  // rows of the item
-  const size_t sf = slot_floats(a.rows, DH);
-  const float* first = a.slots + (2 * mk.c0 + mk.late) * sf;
-  const float* rest = a.slots + 2 * mk.c0 * sf;  // segment x > 0 is in slot 2 (c0 + x)
+  const PagedAttnArgs& a = ma.a;
+  const Mark mk = ma.marks[blockIdx.x + 1];
+  if constexpr (sizeof(T) == 2) {
+    if (any_odd(ma.marks, ma.grid)) {  // the same in every warp
+      attend_all<DH>(a);
+      return;
+    }
+  }
+  const int G = a.Hq / a.p.Hkv;
+  const int last = mk.tokens * G;  // rows of the item
+  const size_t sf = slot_floats(ma.rows, DH);
+  const float* first = ma.slots + (2 * mk.c0 + mk.late) * sf;
+  const float* rest = ma.slots + 2 * mk.c0 * sf;  // segment x > 0 is in slot 2 (c0 + x)
   for (int e = threadIdx.x; e < kPairs; e += kMergeThreads) {
     // consecutive threads: rows first in the quads layout, values of a row first in the other
     const int quad = kQuads ? e / kMergeRows : e % (DH / 4);
     const int r = blockIdx.y * kMergeRows + (kQuads ? e % kMergeRows : e / (DH / 4));
     if (r >= last) continue;
-    const int ml_at = a.rows * DH + 2 * r, v_at = kQuads ? (quad * a.rows + r) * 4 : r * DH + quad * 4;
+    const int ml_at = ma.rows * DH + 2 * r, v_at = kQuads ? (quad * ma.rows + r) * 4 : r * DH + quad * 4;
     float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
     for (int x0 = 0; x0 < mk.n; x0 += kAtOnce) {
       float2 ml[kAtOnce];
@@ -246,14 +334,14 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(MergeArgs a) {
 #pragma unroll
       for (int j = 0; j < kAtOnce; ++j)
         if (x0 + j < mk.n) top = fmaxf(top, ml[j].x);
-      const float corr = l == 0.f ? 0.f : exp2f((m - top) * a.unit_log2);
+      const float corr = l == 0.f ? 0.f : exp2f((m - top) * ma.unit_log2);
       l *= corr;
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[i] *= corr;
 #pragma unroll
       for (int j = 0; j < kAtOnce; ++j) {
         if (x0 + j >= mk.n) continue;
-        const float w = ml[j].y == 0.f ? 0.f : exp2f((ml[j].x - top) * a.unit_log2);  // sum 0: no key was visible
+        const float w = ml[j].y == 0.f ? 0.f : exp2f((ml[j].x - top) * ma.unit_log2);  // sum 0: no key was visible
         l += w * ml[j].y;
         acc[0] += w * v[j].x;
         acc[1] += w * v[j].y;
@@ -264,7 +352,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(MergeArgs a) {
     }
     const bool seen = l != 0.f;
     const float inv = seen ? 1.f / l : 0.f;
-    const int tl = r / a.G, h = mk.g * a.G + (r - tl * a.G);
+    const int tl = r / G, h = mk.g * G + (r - tl * G);
     const int64_t row = mk.row + tl;
     T* dst = reinterpret_cast<T*>(a.O) + (row * a.Hq + h) * DH + quad * 4;
     if constexpr (sizeof(T) == 4)
@@ -273,7 +361,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(MergeArgs a) {
       *reinterpret_cast<uint2*>(dst) =
           make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
     if (a.lse && quad == 0)
-      a.lse[(int64_t)h * a.N + row] = seen ? (m * a.unit_log2 + log2f(l)) * 0.69314718055994531f : -INFINITY;
+      a.lse[(int64_t)h * a.p.N + row] = seen ? (m * ma.unit_log2 + log2f(l)) * 0.69314718055994531f : -INFINITY;
   }
 }
 
@@ -292,8 +380,7 @@ cudaError_t f32_t(const PagedAttnArgs& a, int TB, cudaStream_t s) {
   count_launch();
   e = launch_pdl(paged_f32_kernel<DH, RPT>, dim3((unsigned)grid), dim3(kF32Threads), sizeof(S), s, a, TB, marks, slots);
   if (e != cudaSuccess) return e;
-  MergeArgs m{marks, slots, a.p.N, S::RB, a.Hq / a.p.Hkv, a.Hq, a.scale * 1.4426950408889634f, a.O, a.lse};
-  return launch_merge(MSA_F32, DH, false, m, grid, s);
+  return launch_merge(MSA_F32, false, MergeArgs{a, marks, slots, grid, S::RB, a.scale * 1.4426950408889634f}, s);
 }
 
 // Few rows per KV head: the kernels that hold at most 16 of them.
@@ -301,14 +388,14 @@ bool few_rows(int Hq, int Hkv, int max_q) { return (int64_t)(Hq / Hkv) * max_q <
 
 }  // namespace
 
-cudaError_t launch_merge(msa_dtype dt, int d, bool quads, const MergeArgs& a, int grid, cudaStream_t s) {
-  if (grid < 2) return cudaSuccess;
-  const dim3 g((unsigned)(grid - 1), (unsigned)((a.rows + kMergeRows - 1) / kMergeRows));
+cudaError_t launch_merge(msa_dtype dt, bool quads, const MergeArgs& m, cudaStream_t s) {
+  const int d = m.a.d;
   auto k = dt == MSA_F32 ? (d == 64 ? merge_kernel<float, 64, false> : merge_kernel<float, 128, false>)
            : !quads      ? merge_kernel<__nv_bfloat16, 128, false>
                          : (d == 64 ? merge_kernel<__nv_bfloat16, 64, true> : merge_kernel<__nv_bfloat16, 128, true>);
+  const dim3 grid((unsigned)(m.grid - 1), (unsigned)((m.rows + kMergeRows - 1) / kMergeRows));
   count_launch();
-  return launch_pdl(k, g, dim3(kMergeThreads), 0, s, a);
+  return launch_pdl(k, grid, dim3(kMergeThreads), 0, s, m);
 }
 
 }  // namespace paged

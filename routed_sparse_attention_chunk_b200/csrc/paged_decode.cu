@@ -66,7 +66,7 @@ struct DLayout {
   static constexpr int kQ = kMaxRows * kDH * 2;       // Q rows, K-major, 128-byte swizzle (two buffers)
   static constexpr int kP = kMaxRows * kKeys * 2;     // P^T rows (query rows x keys); two buffers
   static constexpr int kRed = 2 * kMaxRows * 4 * 4;    // [maxima, sums][rows][4 warps]
-  static constexpr int kSmem = 1024 + kStages * kStage + 2 * kQ + 2 * kP + kRed + 8 * 18 + (int)sizeof(Start);
+  static constexpr int kSmem = 1024 + kStages * kStage + 2 * kQ + 2 * kP + kRed + 8 * 19 + (int)sizeof(Start);
   static_assert(kSmem <= 232448, "shared memory of one CTA");
   static constexpr uint32_t kTmemCols = 64;           // S0, S1, O (16 columns each)
 };
@@ -123,7 +123,8 @@ paged_decode_kernel(const __grid_constant__ TileMaps maps, DecParams a) {
   uint64_t* drain = bars + 15;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 16);
   volatile int* abort_s = reinterpret_cast<volatile int*>(bars + 17);
-  Start* start = reinterpret_cast<Start*>(bars + 18);
+  volatile int* odd_s = abort_s + 1;  // a value that is not finite (row_not_finite)
+  Start* start = reinterpret_cast<Start*>(bars + 19);
 
   const PagedBatch& p = a.p;
   const Split sp{p.max_q, kItemCost, kSlack};  // one block of tokens per sequence
@@ -144,6 +145,7 @@ paged_decode_kernel(const __grid_constant__ TileMaps maps, DecParams a) {
     }
     mbar_init(drain, 1);
     *abort_s = 0;
+    *odd_s = 0;
     fence_mbar_init();
   }
   // a programmatic dependent: nothing an earlier kernel writes is read before this wait
@@ -151,7 +153,10 @@ paged_decode_kernel(const __grid_constant__ TileMaps maps, DecParams a) {
   find_start(p, sp, blockIdx.x, gridDim.x, blockIdx.x == 0, start, reinterpret_cast<ScanScratch*>(red_s));
   if (tid == 0) leave_mark(start, sp, blockIdx.x, a.marks + blockIdx.x);
   pdl_trigger();
-  if (!start->any) return;
+  if (!start->any) {
+    if (threadIdx.x == 0) say_odd(a.marks, gridDim.x, blockIdx.x, 0);
+    return;
+  }
   if (warp == 1) {
     tmem_alloc(tmem_slot, DLayout::kTmemCols);
     tmem_relinquish();
@@ -346,12 +351,13 @@ paged_decode_kernel(const __grid_constant__ TileMaps maps, DecParams a) {
                             : (key < pos0 ? 0 : min(key - pos0, kR) * a.G);
 #pragma unroll
         for (int r = 0; r < kR; ++r) sc[r] = r >= low && r < rows ? sc[r] * a.scale_log2 : -INFINITY;
-        // Rows of V past the sequence's end: zeros (see above).  The copy that filled the
-        // stage has landed (S read the same barrier's K); this wait makes it visible here.
-        if (!mem && w.s.len - (key - r_lane) < kKeys) {
-          const uint32_t st = g % kStages;
-          hold(&kv_full[st], (g / kStages) & 1);
-          if (key >= w.s.len) zero_row<kDH>(ring + st * DLayout::kStage + DLayout::kTile, r_lane);
+        // Rows of V that not every query row sees (paged_tma.cuh).  The copy that filled the stage
+        // has landed (S read the same barrier's K); this wait makes it visible here.
+        if (mem ? __any_sync(0xffffffffu, low > 0) : key - r_lane + kKeys - 1 > pos0) {
+          hold(&kv_full[g % kStages], (g / kStages) & 1);
+          uint8_t* vt = ring + (g % kStages) * DLayout::kStage + DLayout::kTile;
+          if (mem ? low > 0 : key >= w.s.len) zero_row<kDH>(vt, r_lane);
+          else if (!mem && key > pos0 && row_not_finite<kDH>(vt, r_lane)) *odd_s = 1;
           __syncwarp();
         }
         // The maximum moves only where a score passes it by 2^8 (always in the first tile with a
@@ -467,7 +473,10 @@ paged_decode_kernel(const __grid_constant__ TileMaps maps, DecParams a) {
     tc_fence_after();
     tmem_dealloc(tmem, DLayout::kTmemCols);
   }
-  if (tid == 0 && *abort_s) raise_flag(p.err_flag, MSA_FLAG_TIMEOUT);
+  if (tid == 0) {
+    if (*abort_s) raise_flag(p.err_flag, MSA_FLAG_TIMEOUT);
+    say_odd(a.marks, gridDim.x, blockIdx.x, *odd_s);
+  }
 }
 
 }  // namespace
@@ -497,8 +506,7 @@ cudaError_t launch_paged_decode(const PagedAttnArgs& a, cudaStream_t s) {
   count_launch();
   e = launch_pdl(kern, dim3((unsigned)grid), dim3(kThreads), (size_t)DLayout::kSmem, s, maps, d);
   if (e != cudaSuccess) return e;
-  MergeArgs m{d.marks, d.slots, a.p.N, d.R, G, a.Hq, 1.f, a.O, a.lse};
-  return launch_merge(MSA_BF16, kDH, false, m, grid, s);
+  return launch_merge(MSA_BF16, false, MergeArgs{a, d.marks, d.slots, grid, d.R, 1.f}, s);
 }
 
 }  // namespace msa

@@ -21,7 +21,8 @@
 // A tile's K and V arrive as one box per page, straight from the block table's
 // pages, or per run of bank rows of the segment plan (paged_tma.cuh), K and V from a
 // warp each, in rings of three.  Rows past the sequence's end are masked, and their
-// V rows zeroed in shared memory before the product.
+// V rows zeroed in shared memory before the product; what a query row does not see
+// never reaches it, whatever it holds (paged_tma.cuh).
 // Persistent: one CTA per SM walks its equal share of all (item, tile) pairs
 // (paged_sched.cuh).  The pipeline runs through item borders: the next item's Q
 // rows wait in shared memory, and move to tensor memory as soon as the current
@@ -72,7 +73,7 @@ struct Layout {
   static constexpr int kKV = 3;                // stages of the K ring and of the V ring
   static constexpr int kQ = kRows * DH * 2;    // the next item's query rows on their way to tensor memory
   static constexpr int kK = Tile<DH>::kBytes;  // one K (or V) tile
-  static constexpr int kBars = 30;
+  static constexpr int kBars = 31;  // and tensor memory's address, the stop flag, the odd flag
   static constexpr int kRowState = kRows * 4 + kRows * 8;  // O's references; one warpgroup's (reference, sum)
   static constexpr int kSmem = 1024 + kQ + 2 * kKV * kK + 8 * kBars + kRowState + (int)sizeof(Start);
   static constexpr uint32_t kTmemCols = 512;   // S0, S1 (128 each), O (DH), P (64), Q (DH / 2)
@@ -143,9 +144,10 @@ paged_prefill_kernel(const __grid_constant__ TileMaps maps, PreParams a) {
   uint64_t* l_ready = o_read + 1;          // [4 warps] the sums of the warpgroup without the last tile
   uint64_t* drain_s = l_ready + 4;
   uint64_t* drain_pv = drain_s + 1;
-  static_assert(4 * kKV + 4 + 3 + 8 <= L::kBars - 1, "barriers");
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + L::kBars - 1);
+  static_assert(4 * kKV + 4 + 3 + 8 <= L::kBars - 2, "barriers");
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + L::kBars - 2);
   volatile int* abort_s = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* odd_s = abort_s + 1;  // a value that is not finite (row_not_finite)
   float* m_s = reinterpret_cast<float*>(bars + L::kBars);     // [kRows] O's references, log2 domain
   float2* ml_s = reinterpret_cast<float2*>(m_s + kRows);      // [kRows] (reference, sum)
   Start* start = reinterpret_cast<Start*>(ml_s + kRows);
@@ -173,6 +175,7 @@ paged_prefill_kernel(const __grid_constant__ TileMaps maps, PreParams a) {
     mbar_init(drain_s, 1);
     mbar_init(drain_pv, 1);
     *abort_s = 0;
+    *odd_s = 0;
     fence_mbar_init();
   }
   // a programmatic dependent: nothing an earlier kernel writes is read before this wait
@@ -180,7 +183,10 @@ paged_prefill_kernel(const __grid_constant__ TileMaps maps, PreParams a) {
   find_start(p, sp, blockIdx.x, gridDim.x, blockIdx.x == 0, start, reinterpret_cast<ScanScratch*>(m_s));
   if (threadIdx.x == 0) leave_mark(start, sp, blockIdx.x, a.marks + blockIdx.x);
   pdl_trigger();
-  if (!start->any) return;
+  if (!start->any) {
+    if (threadIdx.x == 0) say_odd(a.marks, gridDim.x, blockIdx.x, 0);
+    return;
+  }
   if (warp == 1) {
     tmem_alloc(tmem_slot, L::kTmemCols);
     tmem_relinquish();
@@ -359,6 +365,7 @@ paged_prefill_kernel(const __grid_constant__ TileMaps maps, PreParams a) {
       const int seen = w.s.len - w.s.nq + (rvalid ? t : min(w.i * TB + TB, w.s.nq) - 1) + 1;
       // the owner of the item's last tile sees to the next item's Q
       const bool next_q = ((g0 + n - 1) & 1) == (uint32_t)wg && w.f + n < w.f1;
+      const int first = w.s.len - w.s.nq + w.i * TB;  // position of the block's first token
       const int j0 = (int)((g0 ^ wg) & 1);
       float m = -INFINITY, l_run = 0.f;  // this warpgroup's reference maximum (a whole number) and row sum
       for (int j = j0; j < n; j += 2) {
@@ -378,8 +385,7 @@ paged_prefill_kernel(const __grid_constant__ TileMaps maps, PreParams a) {
         }
         if (next_q && j == n - 1) place_q();  // the item's last S is done: Q's columns are free
         float s[kKeys];
-#pragma unroll
-        for (int c = 0; c < kKeys; c += 16) tmem_ld16(tS0 + lane_off + st * kKeys + c, *reinterpret_cast<float(*)[16]>(&s[c]));
+        tmem_ld128(tS0 + lane_off + st * kKeys, s);
         tmem_ld_wait();
         tc_fence_before();
         mbar_arrive(&s_free[st]);
@@ -394,6 +400,12 @@ paged_prefill_kernel(const __grid_constant__ TileMaps maps, PreParams a) {
               const uint32_t cnt = (cw[c >> 5] >> (((c >> 3) & 3) * 8)) & 0xffu;
               s[c] = (uint32_t)(c & 7) < cnt ? s[c] : -INFINITY;
             }
+            const uint32_t vs = g % kKV;
+            hold(&v_full[vs], (g / kKV) & 1);  // see below
+            if ((uint32_t)(r & 7) >= ((q == 0 ? cw[0] : q == 1 ? cw[1] : q == 2 ? cw[2] : cw[3]) >> ((lane >> 3) * 8) & 0xffu))
+              zero_row<DH>(Vs + vs * L::kK, r);
+            fence_async_smem();
+            __syncwarp();
           }
         } else {
           const int base = (tile - w.s.nm) * kKeys;
@@ -402,12 +414,15 @@ paged_prefill_kernel(const __grid_constant__ TileMaps maps, PreParams a) {
 #pragma unroll
             for (int c = 0; c < kKeys; ++c) s[c] = c < lim ? s[c] : -INFINITY;
           }
-          // rows of V past the sequence's end: zeros, before this tile's PV
-          const int end = w.s.len - base;
-          if (end < kKeys) {
+          // Rows of V that not every row of the block sees (tile_row).  The copy that filled the
+          // stage has landed (S read K of the same tile, not V): this wait makes it visible here.
+          if (base + kKeys - 1 > first) {
             const uint32_t vs = g % kKV;
             hold(&v_full[vs], (g / kKV) & 1);
-            if (r >= end) zero_row<DH>(Vs + vs * L::kK, r);
+            uint8_t* vt = Vs + vs * L::kK;
+            const int key = base + r;
+            if (key >= w.s.len) zero_row<DH>(vt, r);
+            else if (key > first && row_not_finite<DH>(vt, r)) *odd_s = 1;
             fence_async_smem();
             __syncwarp();
           }
@@ -560,7 +575,10 @@ paged_prefill_kernel(const __grid_constant__ TileMaps maps, PreParams a) {
     tc_fence_after();
     tmem_dealloc(tmem, L::kTmemCols);
   }
-  if (threadIdx.x == 0 && *abort_s) raise_flag(p.err_flag, MSA_FLAG_TIMEOUT);
+  if (threadIdx.x == 0) {
+    if (*abort_s) raise_flag(p.err_flag, MSA_FLAG_TIMEOUT);
+    say_odd(a.marks, gridDim.x, blockIdx.x, *odd_s);
+  }
 }
 
 template <int DH>
@@ -589,8 +607,7 @@ cudaError_t prefill_t(const PagedAttnArgs& a, cudaStream_t s) {
   count_launch();
   e = launch_pdl(paged_prefill_kernel<DH>, dim3((unsigned)grid), dim3(kThreads), (size_t)L::kSmem, s, maps, d);
   if (e != cudaSuccess) return e;
-  MergeArgs m{d.marks, d.slots, a.p.N, kRows, G, a.Hq, 1.f, a.O, a.lse};
-  return launch_merge(MSA_BF16, DH, true, m, grid, s);
+  return launch_merge(MSA_BF16, true, MergeArgs{a, d.marks, d.slots, grid, kRows, 1.f}, s);
 }
 
 }  // namespace

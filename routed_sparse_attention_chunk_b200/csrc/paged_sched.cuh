@@ -391,9 +391,28 @@ __device__ __forceinline__ void leave_mark(const Start* st, const Split& sp, int
   *m = v;
 }
 
-// Workspace: one Mark per CTA, then two partial results per CTA.  A partial result of `rows`
+// Workspace: one Mark per CTA, one byte per CTA (whether it met values that are not finite among
+// keys that only some rows see), then two partial results per CTA.  A partial result of `rows`
 // rows is rows x DH unnormalised output values and rows x (row maximum, row sum), as floats.
-__host__ __device__ inline size_t marks_bytes(int grid) { return ((size_t)grid * sizeof(Mark) + 255) / 256 * 256; }
+__host__ __device__ inline size_t marks_bytes(int grid) {
+  return ((size_t)grid * (sizeof(Mark) + 1) + 16 + 255) / 256 * 256;
+}
+static_assert(sizeof(Mark) % 16 == 0, "the bytes after the marks are read 16 at a time");
+// One thread of CTA c; the bytes up to the next multiple of 16 are cleared by the last CTA.
+__device__ __forceinline__ void say_odd(Mark* marks, int grid, int c, int odd) {
+  uint8_t* w = reinterpret_cast<uint8_t*>(marks + grid);
+  w[c] = odd != 0;
+  if (c == grid - 1)
+    for (int i = grid; i & 15; ++i) w[i] = 0;
+}
+// One warp, after the kernel that left them: whether any of at most 512 is set.
+__device__ __forceinline__ bool any_odd(const Mark* marks, int grid) {
+  const uint4* w = reinterpret_cast<const uint4*>(marks + grid);
+  const int lane = threadIdx.x & 31;
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if (lane * 16 < grid) v = w[lane];
+  return __any_sync(0xffffffffu, (v.x | v.y | v.z | v.w) != 0);
+}
 __host__ __device__ inline size_t slot_floats(int rows, int dh) {
   return ((size_t)rows * (dh + 2) + 3) / 4 * 4;
 }
@@ -401,19 +420,18 @@ __host__ __device__ inline size_t slot_floats(int rows, int dh) {
 // segments can belong to cut items).
 __device__ __forceinline__ int64_t slot_of(int64_t c, int64_t f, int64_t f0) { return 2 * c + (f == f0 ? 0 : 1); }
 
-// The merging kernel (paged_attn.cu): O and lse of the items the marks name.
+// The merging kernel (paged_attn.cu): O and lse of the items the marks name, or of the whole batch
+// if a CTA says odd.
 struct MergeArgs {
-  const Mark* marks;
+  PagedAttnArgs a;
+  Mark* marks;
   const float* slots;
-  int64_t N;
-  int rows, G, Hq;
+  int grid, rows;   // CTAs that left marks, rows of a slot
   float unit_log2;  // row maxima times this are in the log2 domain
-  void* O;
-  float* lse;
 };
 // quads: values (row, x) of a slot at (x / 4) * rows * 4 + row * 4 + x % 4 (a row per thread
 // writes them coalesced), else at row * DH + x.
-cudaError_t launch_merge(msa_dtype dt, int d, bool quads, const MergeArgs& a, int grid, cudaStream_t s);
+cudaError_t launch_merge(msa_dtype dt, bool quads, const MergeArgs& m, cudaStream_t s);
 
 }  // namespace paged
 }  // namespace msa

@@ -116,15 +116,36 @@ __device__ __forceinline__ void load_box(uint8_t* tile, const CUtensorMap* pages
                        g * pm.h3 + (x.in_page >> 3) * pm.r3, x.at, bar);
 }
 
-// Row r of a V tile set to zeros (a row past the sequence's end: 0 x NaN is NaN, and a page's
-// tail holds anything).
+// Rows of a V tile that some query row must not see although its weight is 0 there: 0 x NaN and
+// 0 x infinity are NaN.  A row that nobody sees (past the sequence's end, where a page holds
+// anything, or padding of a bank run) is set to zeros before the product.  A row that some see and
+// others do not is tested for values that are not finite; a CTA that meets one says so in its
+// mark, and the merging kernel then computes the whole batch on the CUDA cores, which leave out
+// what a row does not see.  (A slow path for such values inside the tile loop cost the loop 10%
+// even where it was not taken.)
+template <int DH>
+__device__ __forceinline__ uint8_t* tile_row(uint8_t* tile, int r) {
+  return tile + (r >> 3) * Tile<DH>::kGroup + (r & 7) * 128;
+}
 template <int DH>
 __device__ __forceinline__ void zero_row(uint8_t* tile, int r) {
-  uint8_t* v = tile + (r >> 3) * Tile<DH>::kGroup + (r & 7) * 128;
+  uint8_t* v = tile_row<DH>(tile, r);
 #pragma unroll
   for (int c = 0; c < 8 * Tile<DH>::kBlocks; ++c)
-    *reinterpret_cast<uint4*>(v + (c >> 3) * 1024 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+    *reinterpret_cast<uint4*>(v + (c >> 3) * 1024 + ((c ^ r) & 7) * 16) = make_uint4(0, 0, 0, 0);
 }
-
+template <int DH>
+__device__ __forceinline__ bool row_not_finite(uint8_t* tile, int r) {
+  const uint8_t* v = tile_row<DH>(tile, r);
+  uint32_t top = 0;  // bit 15 or 31: an exponent of ones carried out
+#pragma unroll
+  for (int c = 0; c < 8 * Tile<DH>::kBlocks; ++c) {
+    const uint4 u = *reinterpret_cast<const uint4*>(v + (c >> 3) * 1024 + ((c ^ r) & 7) * 16);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top |= (w[i] & 0x7f807f80u) + 0x00800080u;
+  }
+  return (top & 0x80008000u) != 0;
+}
 }  // namespace paged
 }  // namespace msa

@@ -272,6 +272,65 @@ def test_agrees_with_the_dense_layer_attention():
     assert ((lse.double() - lse2.transpose(0, 1).reshape(Hq, B * T).double()).abs() <= 2 * bl).all()
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("q_len,total,d,max_q", [
+    ([3], [300], 128, None), ([4, 1], [131, 90], 128, None), ([2], [2], 128, None),     # drafts
+    ([70], [70], 128, None), ([200, 9], [640, 9], 128, None), ([150], [300], 64, None),  # parts of prompts
+    ([3, 4], [257, 128], 128, 90)])
+def test_values_that_are_not_finite(dtype, q_len, total, d, max_q):
+    """Infinities and NaN in V of new tokens reach exactly the tokens that see them, dimension by
+    dimension; in K, the tokens that see the key; in bank rows nobody selected, nobody."""
+    inf, nan = float("inf"), float("nan")
+    b = Batch(q_len, total, 8, 2, d, 16, dtype, DEV, seed=21).select(2, 12, 9, seed=3)
+    Mmax = 18
+    O0, lse0, _ = b.run(Mmax, max_q=max_q)
+    b.check(O0, lse0, Mmax)
+    picked = {c for i in range(len(q_len)) for c in b.memory(i, Mmax)[0]}
+    rest = [c for c in range(b.Kbar.shape[0]) if c not in picked]
+    b.Kbar[rest], b.Vbar[rest] = nan, inf
+    marks = []  # (sequence, position, KV head, dimension, value)
+    for i, (n, t) in enumerate(zip(q_len, total)):
+        for back, g, x, val in ((1, 0, 3, inf), (1, 1, 5, nan), (n // 2 + 1, 0, 7, -inf), (n // 2 + 1, 0, 3, inf),
+                                (n, 1, 60, inf), (max(n // 3, 1), 1, 60, -inf)):
+            if back <= n and (i, t - back, g, x) not in [m[:4] for m in marks]:
+                marks.append((i, t - back, g, x, val))
+    clean = [v.clone() for v in b.vd]
+    want, lo, A = None, None, None
+    for i, pos, g, x, val in marks:
+        clean[i][pos, g, x] = 0
+        pg, row = b.slots(i, torch.tensor([pos]))
+        b.V[pg, row, g, x] = val
+    b.vd = clean
+    want, lo, A = b.attention64(Mmax)
+    bo, bl = b.bounds(want, A, lo, max(total) + Mmax)
+    for i, pos, g, x, val in marks:
+        first = b.off[i] + max(0, pos - (total[i] - q_len[i]))
+        want[first:b.off[i + 1], 4 * g:4 * g + 4, x] += val  # inf - inf: NaN
+    for _ in range(2):
+        O, lse, flag = b.run(Mmax, max_q=max_q)
+        assert _flag(flag) == 0
+        odd = ~want.isfinite()
+        got = O[:b.N].double()
+        assert torch.equal(got.isnan()[odd], want.isnan()[odd])
+        there = odd & ~want.isnan()
+        assert torch.equal(got[there], want[there])
+        assert (got - want).abs()[~odd].le(bo[~odd]).all()
+        assert ((lse[:, :b.N].double() - lo).abs() <= bl).all()
+    # a key that is not finite: its own token and the later ones, of its KV head
+    i = 0
+    b2 = Batch(q_len, total, 8, 2, d, 16, dtype, DEV, seed=21)
+    pos = total[i] - 1 - q_len[i] // 2
+    pg, row = b2.slots(i, torch.tensor([pos]))
+    O1, _, _ = b2.run(max_q=max_q)
+    b2.K[pg, row, 1, 2] = nan
+    O2, _, flag = b2.run(max_q=max_q)
+    assert _flag(flag) == 0
+    first = b2.off[i] + pos - (total[i] - q_len[i])
+    hit = torch.zeros(b2.N, 8, dtype=torch.bool, device=DEV)
+    hit[first:b2.off[i + 1], 4:] = True
+    assert O2[:b2.N][hit].isnan().all() and torch.equal(O2[:b2.N][~hit], O1[:b2.N][~hit])
+
+
 def test_launches_are_counted():
     b = Batch([1, 1], [40, 30], 8, 2, 128, 16, BF, DEV, seed=17)
     n = msa.kernel_launch_count()
