@@ -639,6 +639,7 @@ msa_status msa_paged_append(msa_dtype dt, const void* q, int64_t q_tok_stride, v
  * Supported: Hq % Hkv == 0, at most 64 query heads per KV head.  bf16 runs on the
  * tensor cores, fp32 in fp32.  The result does not depend on timing: partial sums
  * are merged in a fixed order.
+ * O and lse must not overlap the inputs.
  * Workspace: msa_paged_attn_workspace_size bytes (for the same arguments and the
  * device that runs the call current), 16-byte aligned, not initialised, not kept;
  * calls that may overlap on the GPU need one each.

@@ -284,7 +284,8 @@ def gated_delta_rule(q, k, v, g, beta, o, h0=None, hT=None, scale=0.0, stream=No
 
 
 # ---- rotary positions and the paged cache of the local keys and values
-# A decoding step calls these for every layer, so each tensor is looked at once.
+# A decoding step calls these for every layer, so each tensor is looked at once.  All tensors are on
+# the current device (one on another is refused), and the work goes to its current stream or `stream`.
 
 
 # The first line of each check is the whole of it for a good tensor; what is wrong is found after.

@@ -223,8 +223,8 @@ msa_status check_paged(msa_dtype dt, int64_t N, int64_t B, const int64_t* q_off,
   if (N == 0 || B == 0) return MSA_OK;  // nothing to read: pointers of empty tensors may be NULL
   if (!q_off || !K || !V || !table || !seq_len) return MSA_ERR_INVALID_ARG;
   if (!aligned16(K) || !aligned16(V)) return MSA_ERR_INVALID_ARG;
-  if (!vec_stride(dt, page_stride) || !vec_stride(dt, row_stride) || !vec_stride(dt, head_stride) ||
-      !strides_apart(d, page_stride, num_pages, row_stride, page, head_stride, Hkv))
+  if ((num_pages > 1 && !vec_stride(dt, page_stride)) || !vec_stride(dt, row_stride) ||
+      (Hkv > 1 && !vec_stride(dt, head_stride)) || !strides_apart(d, page_stride, num_pages, row_stride, page, head_stride, Hkv))
     return MSA_ERR_INVALID_ARG;
   return MSA_OK;
 }
@@ -714,7 +714,8 @@ msa_status msa_paged_append(msa_dtype dt, const void* q, int64_t q_tok_stride, v
     if (Hq > 65535) return MSA_ERR_UNSUPPORTED;
   }
   PagedAppendArgs a{};
-  a.p = PagedBatch{q_off, seq_len, block_table, nullptr, N, B, 0, max_pages, page, 0, Hkv, num_pages, err_flag};
+  a.p = PagedBatch{q_off, seq_len, block_table, nullptr, N, B, (int)kMaxIndex, max_pages, page, 0, Hkv, num_pages,
+                   err_flag};
   a.q = q;
   a.k = k;
   a.v = v;

@@ -11,6 +11,7 @@
 // chain of dependent loads) is found while they are in flight.
 #include "common.cuh"
 #include "internal.h"
+#include "paged_seq.cuh"
 #include "rope.cuh"
 
 namespace msa {
@@ -22,6 +23,8 @@ __global__ void __launch_bounds__(kRopeThreads) paged_append_kernel(PagedAppendA
   const PagedBatch& p = a.p;
   const int Hkv = p.Hkv, Hq = a.q ? a.Hq : 0, heads = Hq + 2 * Hkv;
   const int64_t id = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (blockIdx.x == 0 && p.err_flag)  // offsets and lengths that do not fit the arguments
+    for (int64_t b = threadIdx.x; b < p.B; b += blockDim.x) paged::load_seq(p, b, p.err_flag);
   if (id >= total) return;
   const uint32_t per = (uint32_t)(units * groups);
   const int64_t n = total < 0xffffffffll ? (int64_t)((uint32_t)id / per) : id / per;
@@ -56,10 +59,7 @@ __global__ void __launch_bounds__(kRopeThreads) paged_append_kernel(PagedAppendA
     }
   }
   const int64_t q0 = __ldg(p.q_off + lo), q1 = __ldg(p.q_off + lo + 1);
-  if (n < q0 || n >= q1) {  // a row behind the last sequence, or offsets that do not ascend from 0
-    if (report && n < q0) raise_flag(p.err_flag, MSA_FLAG_OFFSETS);
-    return;
-  }
+  if (n < q0 || n >= q1) return;  // a row outside every sequence
   const int64_t at = (int64_t)__ldg(p.seq_len + lo) - (q1 - n);  // cache position
   if (q1 > p.N || at < 0) {
     if (report) raise_flag(p.err_flag, MSA_FLAG_OFFSETS);

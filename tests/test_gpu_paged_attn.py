@@ -331,6 +331,38 @@ def test_values_that_are_not_finite(dtype, q_len, total, d, max_q):
     assert O2[:b2.N][hit].isnan().all() and torch.equal(O2[:b2.N][~hit], O1[:b2.N][~hit])
 
 
+@pytest.mark.parametrize("dtype,max_q", [(F32, 1), (BF, 1), (BF, 40)])
+def test_no_new_tokens_at_all(dtype, max_q):
+    """Sequences without new tokens leave everything as it was; rows before the first are nobody's."""
+    b = Batch([0, 0, 0], [30, 0, 7], 8, 2, 128, 16, dtype, DEV, seed=22, pad_rows=4)
+    O, lse, flag = b.run(max_q=max_q)
+    assert _flag(flag) == 0 and (O == 7).all() and (lse == 7).all()
+    b = Batch([1, 1], [30, 70], 8, 2, 128, 16, dtype, DEV, seed=22, pad_rows=2)
+    b.Q = torch.cat([b.Q[2:], b.Q[:2]]).contiguous()
+    b.q_off += 2
+    O, lse, flag = b.run(max_q=max_q)
+    assert _flag(flag) == 0 and (O[:2] == 7).all()
+    b.Q, b.q_off = torch.cat([b.Q[2:], b.Q[:2]]), b.q_off - 2
+    b.check(torch.cat([O[2:], O[:2]]), torch.cat([lse[:, 2:], lse[:, :2]], 1))
+
+
+def test_without_lse():
+    for q_len in ([1, 1], [40, 3]):
+        b = Batch(q_len, [300, 40], 8, 2, 128, 16, BF, DEV, seed=23)
+        O, none, flag = b.run(want_lse=False)
+        assert none is None and _flag(flag) == 0
+        b.check(O, None)
+
+
+def test_a_key_selected_twice():
+    """A document selected twice counts twice, as in msa_sparse_attn_indexed."""
+    b = Batch([1, 60], [30, 90], 8, 2, 128, 16, BF, DEV, seed=24).select(3, 10, 5, seed=1)
+    b.idx[:, 2] = b.idx[:, 0]
+    O, lse, flag = b.run(30)
+    assert _flag(flag) == 0
+    b.check(O, lse, 30)
+
+
 def test_launches_are_counted():
     b = Batch([1, 1], [40, 30], 8, 2, 128, 16, BF, DEV, seed=17)
     n = msa.kernel_launch_count()

@@ -228,7 +228,12 @@ def test_append_skips_and_flags():
     o[3] = 9
     assert run(q_off=o)[0] == msa.FLAG_OFFSETS
     o = b.q_off + 1
+    assert run(q_off=o)[0] == msa.FLAG_OFFSETS  # its last sequence passes the packed rows
+    o = b.q_off.clone()
+    o[1] = 4  # decreasing after it
     assert run(q_off=o)[0] & msa.FLAG_OFFSETS
+    o = torch.tensor([1, 2, 3, 4], device=DEV)  # the first row is nobody's: nothing is wrong
+    assert run(q_off=o)[0] == 0
 
 
 @pytest.mark.parametrize("dtype", [F32, BF])
