@@ -52,14 +52,14 @@ __global__ void __launch_bounds__(kF32Threads) paged_f32_kernel(PagedAttnArgs a,
   const int G = a.Hq / p.Hkv;
   const Split sp{TB, kF32ItemCost, kF32Slack};
   pdl_wait();
-  find_start(p, sp, blockIdx.x, gridDim.x, blockIdx.x == 0, &sm.st, reinterpret_cast<ScanScratch*>(sm.row));
+  find_start<RPT == 1>(p, sp, blockIdx.x, gridDim.x, blockIdx.x == 0, &sm.st, reinterpret_cast<ScanScratch*>(sm.row));
   if (tid == 0) leave_mark(&sm.st, sp, blockIdx.x, marks + blockIdx.x);
   pdl_trigger();
   if (!sm.st.any) return;
   const float sl2 = a.scale * 1.4426950408889634f;
   const float* Q = reinterpret_cast<const float*>(a.Q);
 
-  for (Walk w(sp, &sm.st); w.more(); w.next(p, sp)) {
+  for (WalkT<RPT == 1> w(sp, &sm.st); w.more(); w.next(p, sp)) {
     const Seq& s = w.s;
     const int tb0 = w.i * TB;
     __syncthreads();  // the previous segment's readers are done

@@ -45,6 +45,8 @@ constexpr uint32_t kWaitPolls = 1u << 24;
 constexpr uint32_t kSpinLimit = 1u << 28;  // non-blocking polls of the MMA issuer without progress
 constexpr float kRescaleLog2 = 8.0f;
 
+using Walk = WalkT<true>;  // one block of tokens per sequence
+
 struct DecParams {
   PagedBatch p;
   const __nv_bfloat16* Q;
@@ -150,7 +152,7 @@ paged_decode_kernel(const __grid_constant__ TileMaps maps, DecParams a) {
   }
   // a programmatic dependent: nothing an earlier kernel writes is read before this wait
   pdl_wait();
-  find_start(p, sp, blockIdx.x, gridDim.x, blockIdx.x == 0, start, reinterpret_cast<ScanScratch*>(red_s));
+  find_start<true>(p, sp, blockIdx.x, gridDim.x, blockIdx.x == 0, start, reinterpret_cast<ScanScratch*>(red_s));
   if (tid == 0) leave_mark(start, sp, blockIdx.x, a.marks + blockIdx.x);
   pdl_trigger();
   if (!start->any) {
@@ -442,15 +444,16 @@ paged_decode_kernel(const __grid_constant__ TileMaps maps, DecParams a) {
       bar_softmax();
       const bool whole = w.whole();
       float* slot = a.slots + slot_of(blockIdx.x, w.f, start->f0) * slot_floats(a.R, kDH);
+      int t = 0, hh = 0;  // row r's token and head of the group
 #pragma unroll
       for (int r = 0; r < kR; ++r) {
         if (r >= rows) break;
         const float4 lv = *reinterpret_cast<const float4*>(red_l + r * 4);
         const float l = (lv.x + lv.y) + (lv.z + lv.w);
-        const int t = r / a.G, h = w.g * a.G + r % a.G;
         if (whole) {
           // a sum of 0: no key was visible
           const float inv = l == 0.f ? 0.f : 1.f / l;
+          const int h = w.g * a.G + hh;
           a.O[((w.s.q0 + t) * a.Hq + h) * kDH + r_lane] = __float2bfloat16_rn(l == 0.f ? 0.f : o[r] * inv);
           if (a.lse && et == 0)
             a.lse[(int64_t)h * p.N + w.s.q0 + t] =
@@ -458,6 +461,10 @@ paged_decode_kernel(const __grid_constant__ TileMaps maps, DecParams a) {
         } else {
           slot[r * kDH + r_lane] = o[r];
           if (et == 0) *reinterpret_cast<float2*>(slot + a.R * kDH + 2 * r) = make_float2(m_run[r], l);
+        }
+        if (++hh == a.G) {
+          hh = 0;
+          ++t;
         }
       }
       bar_softmax();

@@ -53,6 +53,8 @@ constexpr int kItemCost = 4, kSlack = 8;  // see Split
 constexpr uint32_t kWaitPolls = 1u << 24;
 constexpr float kRescaleLog2 = 8.0f;  // move the running max only when it grows by more than this
 
+using Walk = WalkT<false>;
+
 struct PreParams {
   PagedBatch p;
   const __nv_bfloat16* Q;
@@ -180,7 +182,7 @@ paged_prefill_kernel(const __grid_constant__ TileMaps maps, PreParams a) {
   }
   // a programmatic dependent: nothing an earlier kernel writes is read before this wait
   pdl_wait();
-  find_start(p, sp, blockIdx.x, gridDim.x, blockIdx.x == 0, start, reinterpret_cast<ScanScratch*>(m_s));
+  find_start<false>(p, sp, blockIdx.x, gridDim.x, blockIdx.x == 0, start, reinterpret_cast<ScanScratch*>(m_s));
   if (threadIdx.x == 0) leave_mark(start, sp, blockIdx.x, a.marks + blockIdx.x);
   pdl_trigger();
   if (!start->any) {

@@ -69,22 +69,16 @@ __device__ __forceinline__ int64_t sum_div_keys(uint32_t n, uint32_t a, uint32_t
   return ans;
 }
 
-// Tiles of blocks [0, n) of a sequence.
+// Tiles of blocks [0, n) of a sequence, n at most the number of its blocks of TB whole tokens.
 __device__ __forceinline__ int64_t tiles_before(const Seq& s, int TB, int n) {
-  const int nb = blocks_of(s, TB);
-  if (nb == 0 || n <= 0) return 0;
-  const bool all = n >= nb;
-  const int m = all ? nb - 1 : n;  // blocks of TB whole tokens
-  int64_t t = 0;
-  if (m > 0) {
-    const int hist = s.len - s.nq;
-    // blocks that end at or before position 0 see no local key
-    const int i0 = hist >= 0 ? 0 : min(m, -hist / TB);
-    t = (int64_t)i0 * max(1, s.nm);
-    if (m > i0)
-      t += (int64_t)(m - i0) * s.nm + sum_div_keys(m - i0, TB, (uint32_t)hist + (uint32_t)((i0 + 1) * TB) + kKeys - 1);
-  }
-  return all ? t + block_tiles(s, TB, nb - 1) : t;
+  if (n <= 0) return 0;
+  const int hist = s.len - s.nq;
+  // blocks that end at or before position 0 see no local key
+  const int i0 = hist >= 0 ? 0 : min(n, -hist / TB);
+  int64_t t = (int64_t)i0 * max(1, s.nm);
+  if (n > i0)
+    t += (int64_t)(n - i0) * s.nm + sum_div_keys(n - i0, TB, (uint32_t)hist + (uint32_t)((i0 + 1) * TB) + kKeys - 1);
+  return t;
 }
 
 // What a kernel's work looks like to the split.
@@ -109,120 +103,48 @@ struct ScanScratch {  // shared memory, free again after find_start
   int counts[16], tops[16];
 };
 
-// The block of sequence q that holds unit `rest`: the last one with no more units before it, 32
-// probes at a time.  A whole warp calls it; every lane gets the answer.
-__device__ __forceinline__ int find_block(const Seq& q, const Split& sp, int64_t rest, int lane) {
-  int lo = 0, n = blocks_of(q, sp.TB);  // answer in [lo, lo + n)
-  while (n > 1) {
-    const int step = (n + 31) >> 5;
-    const int probe = lo + lane * step;
-    const unsigned hit = __ballot_sync(
-        0xffffffffu, lane * step < n && tiles_before(q, sp.TB, probe) + (int64_t)probe * sp.cost <= rest);
-    const int last = 31 - __clz(hit);  // lane 0 always hits
-    lo += last * step;
-    n = min(step, n - last * step);
-  }
-  return lo;
-}
-
-// Where the share begins inside item (g, b, block i): the last part of find_start, by one thread.
-__device__ __forceinline__ void set_start(const Split& sp, int64_t rest, bool one, const Seq& q, int lo, Start* st) {
-  const int o = one ? 0 : (int)(rest - tiles_before(q, sp.TB, lo) - (int64_t)lo * sp.cost);
-  const int T = block_tiles(q, sp.TB, lo);
-  if (one) st->f1 = sp.cost + T;
-  st->i = lo;
-  st->o = o;
-  // a share may hold nothing but the start of an item that the next one takes
-  st->any = min((int64_t)T, o + (st->f1 - st->f0) - sp.cost) > max(0, o - sp.cost);
-}
-
-// find_start for at most 32 sequences whose units all together stay below 2^31: one warp, a
-// sequence per lane, in 32 bits.  False (in every lane) if they do not fit.  A kernel over a short
-// cache spends a good part of its time before its first load (2.3 of 7 us in the general form).
-__device__ __forceinline__ bool find_start_small(const PagedBatch& p, const Split& sp, int64_t c, int64_t grid,
-                                                 bool report, int lane, Start* st) {
-  Seq s{0, 0, 0, 0};
-  if (lane < p.B) s = load_seq(p, lane, report ? p.err_flag : nullptr);
-  const int nb = blocks_of(s, sp.TB);
-  const int last = nb > 0 ? block_tiles(s, sp.TB, nb - 1) : 0;
-  // no block has more keys than the last one
-  if (__any_sync(0xffffffffu, (int64_t)nb * (last + sp.cost) * p.Hkv >= (1 << 25))) return false;
-  const int mine = nb > 0 ? (int)tiles_before(s, sp.TB, nb - 1) + last + nb * sp.cost : 0;
-  int incl = mine, icl = nb;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, incl, o), u = __shfl_up_sync(0xffffffffu, icl, o);
-    if (lane >= o) {
-      incl += v;
-      icl += u;
-    }
-  }
-  const int total = __shfl_sync(0xffffffffu, incl, 31), items = __shfl_sync(0xffffffffu, icl, 31);
-  const int most = __reduce_max_sync(0xffffffffu, last);
-  const int Ttot = total * p.Hkv;
-  const int per = max(1, (int)((uint32_t)(Ttot + (int)grid - 1) / (uint32_t)grid));
-  const bool one = items * p.Hkv <= grid && most + sp.cost <= per + sp.slack;
-  const int64_t f0 = c * per;
-  const bool any = one ? c < items * p.Hkv : f0 < Ttot;
-  if (!any) {
-    if (lane == 0) st->any = 0;
-    return true;
-  }
-  const uint32_t div = one ? items : total, at = one ? (uint32_t)c : (uint32_t)f0;
-  const int g = (int)(at / div), w = (int)(at - g * div);
-  const int lo_w = one ? icl - nb : incl - mine, hi_w = one ? icl : incl;
-  const int b = __ffs(__ballot_sync(0xffffffffu, w >= lo_w && w < hi_w)) - 1;
-  Seq q;
-  q.q0 = __shfl_sync(0xffffffffu, s.q0, b);
-  q.nq = __shfl_sync(0xffffffffu, s.nq, b);
-  q.len = __shfl_sync(0xffffffffu, s.len, b);
-  q.nm = __shfl_sync(0xffffffffu, s.nm, b);
-  const int rest = w - __shfl_sync(0xffffffffu, lo_w, b);
-  const int lo = one ? rest : find_block(q, sp, rest, lane);
-  if (lane == 0) {
-    st->per = per;
-    st->f0 = one ? 0 : f0;
-    st->f1 = min(f0 + per, (int64_t)Ttot);
-    st->g = g;
-    st->b = b;
-    st->s = q;
-    set_start(sp, rest, one, q, lo, st);
-  }
-  return true;
-}
-
-// All threads of the CTA call it (blockDim.x a multiple of 32, at most 512);
-// on return st (shared memory) holds share c of `grid` shares.
+// All threads of the CTA call it (blockDim.x a multiple of 32, at most 512); on return st (shared
+// memory) holds share c of `grid` shares.  kOneBlock: sp.TB covers every sequence.  Up to 32
+// sequences take one warp's shuffles and one barrier (a kernel over a short cache spends a good
+// part of its time before its first load).  The tile counts appear twice in the code only: the
+// kernels' loops run slower the more of it lies around them (decoding 12 rows over 1.13 GB took
+// 193 us with seven copies, 183 with two).
+template <bool kOneBlock>
 __device__ __forceinline__ void find_start(const PagedBatch& p, const Split& sp, int64_t c, int64_t grid,
                                            bool report, Start* st, ScanScratch* sc) {
-  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = nt >> 5;
+  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
   const int TB = sp.TB;
-  if (p.B <= 32) {
-    if (warp == 0) {
-      const bool done = find_start_small(p, sp, c, grid, report, lane, st);
-      if (lane == 0) sc->counts[0] = done;
-    }
-    __syncthreads();
-    if (sc->counts[0]) return;
-    __syncthreads();  // the scratch is written again
-  }
+  const bool one_warp = p.B <= 32;
   const int chunk = (int)(((uint32_t)p.B + nt - 1) / (uint32_t)nt);  // B < 2^31
   const int64_t b0 = min(p.B, (int64_t)tid * chunk), b1 = min(p.B, b0 + chunk);
   int64_t mine = 0;         // units of this thread's sequences
   int items = 0, most = 0;  // their blocks (at most N < 2^31), the tiles of the largest
-  Seq s;
-  for (int64_t b = b0; b < b1; ++b) {
-    s = load_seq(p, b, report ? p.err_flag : nullptr);
-    const int nb = blocks_of(s, TB);
-    mine += tiles_before(s, TB, nb) + (int64_t)nb * sp.cost;
-    items += nb;
-    if (nb > 0) most = max(most, block_tiles(s, TB, nb - 1));  // no block has more keys than the last
-  }
-  // the warps past the last sequence take no part in the scan
-  const int used = (int)min((int64_t)warps, (p.B + 31 * (int64_t)chunk) / (32 * (int64_t)chunk) + 1);
-  int64_t incl = mine;
-  int icl = items;
-  if (warp < used) {
+  int64_t per = 1, f0 = 0, rest = 0, b = b0;
+  bool one = false, any = false, owner = false;
+  int g = 0;
+  Seq s{0, 0, 0, 0};
+  for (int pass = 0;; ++pass) {
+    // pass 0 sums this thread's sequences; pass 1, of the thread that has the share's start among
+    // them, stops at its sequence
+    for (b = b0; b < b1; ++b) {
+      s = load_seq(p, b, report && pass == 0 ? p.err_flag : nullptr);
+      const int nb = kOneBlock ? (s.nq > 0) : blocks_of(s, TB);
+      const int last = nb > 0 ? block_tiles(s, TB, nb - 1) : 0;  // no block has more keys than the last
+      const int64_t units = (kOneBlock ? 0 : tiles_before(s, TB, nb - 1)) + last + (int64_t)nb * sp.cost;
+      if (pass == 0) {
+        mine += units;
+        items += nb;
+        most = max(most, last);
+      } else {
+        const int64_t n = one ? nb : units;
+        if (rest < n) break;
+        rest -= n;
+      }
+    }
+    if (pass == 1) break;
+    if (one_warp && warp > 0) break;
+    int64_t incl = mine;
+    int icl = items;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
@@ -233,76 +155,93 @@ __device__ __forceinline__ void find_start(const PagedBatch& p, const Split& sp,
       }
     }
     most = __reduce_max_sync(0xffffffffu, most);
-    if (lane == 31) {
-      sc->sums[warp] = incl;
-      sc->counts[warp] = icl;
-      sc->tops[warp] = most;
-    }
-  }
-  __syncthreads();
-  int64_t before = 0, total = 0;
-  int ibefore = 0, n_items = 0;
-  most = 0;
-  for (int w = 0; w < used; ++w) {
-    if (w < warp) {
-      before += sc->sums[w];
-      ibefore += sc->counts[w];
-    }
-    total += sc->sums[w];
-    n_items += sc->counts[w];
-    most = max(most, sc->tops[w]);
-  }
-  incl += before;
-  icl += ibefore;
-  const int64_t Ttot = total * p.Hkv;
-  // 32-bit divisions where the numbers allow (64-bit ones cost about a microsecond together)
-  const bool small = Ttot + grid < 0x7fffffff;
-  const int64_t per = max((int64_t)1, small ? (int64_t)((uint32_t)(Ttot + grid - 1) / (uint32_t)grid)
-                                            : (Ttot + grid - 1) / grid);
-  // an item per CTA, if there are no more and none is too long
-  const bool one = (int64_t)n_items * p.Hkv <= grid && most + sp.cost <= per + sp.slack;
-  const int64_t f0 = c * per;
-  const bool any = one ? c < (int64_t)n_items * p.Hkv : f0 < Ttot;
-  // KV head, and the unit (or block) of that head where the share begins
-  const int64_t div = one ? n_items : total, at = one ? c : f0;
-  const int64_t g = !any ? 0 : small ? (int64_t)((uint32_t)at / (uint32_t)div) : at / div;
-  const int64_t w = at - g * div;
-  if (tid == 0) {
-    st->per = per;
-    st->f0 = one ? 0 : f0;
-    st->f1 = min(f0 + per, Ttot);
-    st->g = (int)g;
-    if (!any) st->any = 0;
-  }
-  const int64_t lo_w = one ? icl - items : incl - mine, hi_w = one ? icl : incl;
-  if (any && w >= lo_w && w < hi_w) {  // exactly one thread
-    int64_t rest = w - lo_w, b = b0;
-    if (chunk > 1) {
-      for (;;) {
-        s = load_seq(p, b);
-        const int nb = blocks_of(s, TB);
-        const int64_t n = one ? nb : tiles_before(s, TB, nb) + (int64_t)nb * sp.cost;
-        if (rest < n) break;
-        rest -= n;
-        ++b;
+    int64_t total = __shfl_sync(0xffffffffu, incl, 31);
+    int n_items = __shfl_sync(0xffffffffu, icl, 31);
+    if (!one_warp) {
+      if (lane == 31) {
+        sc->sums[warp] = incl;
+        sc->counts[warp] = icl;
+        sc->tops[warp] = most;
+      }
+      __syncthreads();
+      total = 0;
+      n_items = 0;
+      most = 0;
+      for (int w = 0; w < (nt >> 5); ++w) {
+        if (w == warp) {
+          incl += total;
+          icl += n_items;
+        }
+        total += sc->sums[w];
+        n_items += sc->counts[w];
+        most = max(most, sc->tops[w]);
       }
     }
+    const int64_t Ttot = total * p.Hkv;
+    // 32-bit divisions where the numbers allow (64-bit ones cost about a microsecond together)
+    const bool small = Ttot + grid < 0x7fffffff;
+    per = max((int64_t)1, small ? (int64_t)((uint32_t)(Ttot + grid - 1) / (uint32_t)grid) : (Ttot + grid - 1) / grid);
+    // an item per CTA, if there are no more and none is too long
+    one = (int64_t)n_items * p.Hkv <= grid && most + sp.cost <= per + sp.slack;
+    f0 = c * per;
+    any = one ? c < (int64_t)n_items * p.Hkv : f0 < Ttot;
+    // KV head, and the unit (or block) of that head where the share begins
+    const int64_t div = one ? n_items : total, at = one ? c : f0;
+    g = !any ? 0 : (int)(small ? (int64_t)((uint32_t)at / (uint32_t)div) : at / div);
+    const int64_t w = at - g * div, lo_w = one ? icl - items : incl - mine, hi_w = one ? icl : incl;
+    owner = any && w >= lo_w && w < hi_w;  // exactly one thread
+    rest = w - lo_w;
+    if (tid == 0) {
+      st->per = per;
+      st->f0 = one ? 0 : f0;
+      st->f1 = min(f0 + per, Ttot);
+      st->g = g;
+      if (!any) st->any = 0;
+    }
+    if (!owner) break;
+  }
+  if (owner) {
     st->b = b;
     st->s = s;
     st->rest = rest;
   }
-  __syncthreads();
+  if (one_warp) __syncwarp();
+  else __syncthreads();
   if (any && warp == 0) {
     const Seq q = st->s;
-    const int64_t rest = st->rest;
-    const int lo = one ? (int)rest : find_block(q, sp, rest, lane);
-    if (lane == 0) set_start(sp, rest, one, q, lo, st);
+    const int64_t at = st->rest;
+    int lo = one ? (int)at : 0;
+    int64_t before = 0;  // units of the blocks before `lo`
+    if (!kOneBlock && !one) {
+      // the block holding unit `at`: the last one with no more units before it, 32 probes at a time
+      int n = blocks_of(q, TB);  // answer in [lo, lo + n)
+      while (n > 1) {
+        const int step = (n + 31) >> 5;
+        const int probe = lo + min(lane * step, n - 1);
+        const int64_t units = tiles_before(q, TB, probe) + (int64_t)probe * sp.cost;
+        const unsigned hit = __ballot_sync(0xffffffffu, lane * step < n && units <= at);
+        const int last = 31 - __clz(hit);  // lane 0 always hits
+        before = __shfl_sync(0xffffffffu, units, last);
+        lo += last * step;
+        n = min(step, n - last * step);
+      }
+    }
+    if (lane == 0) {
+      const int o = one ? 0 : (int)(at - before);
+      const int T = block_tiles(q, TB, lo);
+      if (one) st->f1 = sp.cost + T;
+      st->i = lo;
+      st->o = o;
+      // a share may hold nothing but the start of an item that the next one takes
+      st->any = min((int64_t)T, o + (st->f1 - st->f0) - sp.cost) > max(0, o - sp.cost);
+    }
   }
   __syncthreads();
 }
 
 // Walks a CTA's share segment by segment (only if the share has a tile).
-struct Walk {
+template <bool kOneBlock>
+struct WalkT {
   int64_t f, f1, b;
   int g, i, o, t0, T, n;  // item, units of it before f, first tile of the segment, tiles of item and segment
   Seq s;
@@ -312,7 +251,7 @@ struct Walk {
     n = (int)min((int64_t)T, f1 - f + o - sp.cost) - t0;
     if (n <= 0) f = f1;  // the share ends before the item's first tile
   }
-  __device__ __forceinline__ Walk(const Split& sp, const Start* st)
+  __device__ __forceinline__ WalkT(const Split& sp, const Start* st)
       : f(st->f0), f1(st->f1), b(st->b), g(st->g), i(st->i), o(st->o), s(st->s) {
     span(sp);
   }
@@ -323,7 +262,7 @@ struct Walk {
     f += sp.cost + T - o;
     if (f >= f1) return;
     o = 0;
-    if ((int64_t)++i * sp.TB >= s.nq) {
+    if (kOneBlock || (int64_t)++i * sp.TB >= s.nq) {
       i = 0;
       do {
         if (++b == p.B) {
