@@ -48,7 +48,7 @@ using namespace paged;
 
 constexpr int kRows = 128;     // MMA M: query rows per block
 constexpr int kThreads = 384;  // K producer, S issuer, PV issuer, V producer, 2 x 4 softmax warps
-constexpr int kSoftRegs = 216, kOtherRegs = 72;  // 256 x 216 + 128 x 72 = 384 x 168, the launch's registers
+constexpr int kSoftRegs = 208, kOtherRegs = 88;  // 256 x 208 + 128 x 88 = 384 x 168, the launch's registers
 constexpr int kItemCost = 4, kSlack = 8;  // see Split
 constexpr uint32_t kWaitPolls = 1u << 24;
 constexpr float kRescaleLog2 = 8.0f;  // move the running max only when it grows by more than this
