@@ -288,44 +288,38 @@ def gated_delta_rule(q, k, v, g, beta, o, h0=None, hT=None, scale=0.0, stream=No
 # the current device (one on another is refused), and the work goes to its current stream or `stream`.
 
 
-# The first line of each check is the whole of it for a good tensor; what is wrong is found after.
+# Each entry point asks all its questions in one expression; which one failed is found after.
 _cuda_dev = torch._C._cuda_getDevice
 _cuda_stream = torch._C._cuda_getCurrentRawStream
+_I32, _I64, _F32T = torch.int32, torch.int64, torch.float32
 
 
-def _refuse(t, name, dtype, dev, shape):
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is not on the current CUDA device")
-    if t.dtype != dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
-    raise ValueError(f"{name} must be contiguous")
+def _refuse(*tensors):
+    """Raises for the first (tensor, name, dtype, shape, rows) that is not on the current device, of
+    that dtype and shape, and contiguous; rows "last": in its last dimension alone, "heads": rows
+    [N, H, d] whose heads follow one another."""
+    dev = _cuda_dev()
+    for t, name, dtype, shape, rows in tensors:
+        if t is None:
+            continue
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is not on the current CUDA device")
+        if t.dtype != dtype:
+            raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+        st = t.stride()
+        if rows and st[-1] != 1 and shape[-1] > 1:
+            raise ValueError(f"the last dimension of {name} must be contiguous")
+        if rows == "heads" and st[1] != shape[2] and shape[1] > 1:
+            raise ValueError(f"the heads of {name} must be contiguous")
+        if not rows and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
 
 
-def _at(t, name, dtype, dev, shape=None):
-    """Device pointer of a contiguous tensor of this dtype (and shape) on the current device."""
-    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and (shape is None or t.shape == shape):
-        return t.data_ptr()
-    _refuse(t, name, dtype, dev, shape)
-
-
-def _rows_at(t, name, dtype, dev, shape):
-    """Strides of a tensor whose last dimension alone has to be contiguous."""
-    st = t.stride()
-    if t.dtype is dtype and t.get_device() == dev and t.shape == shape and st[-1] == 1:
-        return st
-    if t.shape == shape and shape[-1] == 1 and t.dtype == dtype and t.get_device() == dev:
-        return st
-    _refuse(t, f"the last dimension of {name}" if t.shape == shape else name, dtype, dev, shape)
-
-
-def _heads_at(t, name, dtype, dev, shape):
-    """Token stride of rows [N, H, d] whose heads follow one another."""
-    st = _rows_at(t, name, dtype, dev, shape)
-    if st[1] != shape[2] and shape[1] > 1:
-        raise ValueError(f"the heads of {name} must be contiguous")
-    return st[0]
+def _good(t, dtype, dev, shape):
+    """An optional contiguous tensor: absent, or on the device and of this dtype and shape."""
+    return t is None or (t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous())
 
 
 def rope_table_scaled(method: str, theta: float, rd: int, max_len: int, factor: float = 1.0, orig_len: float = 0.0,
@@ -341,15 +335,20 @@ def rope_table_scaled(method: str, theta: float, rd: int, max_len: int, factor: 
 
 
 def _rope(fn, x, pos, rope_cs, out, layout, err_flag, stream):
-    dt, dev, dtype = _dt(x), _cuda_dev(), x.dtype
+    dtype, dev = x.dtype, _cuda_dev()
+    dt = _dt(x)
     N, H, d = shape = x.shape
-    xs, os = _rows_at(x, "x", dtype, dev, shape), _rows_at(out, "out", dtype, dev, shape)
-    max_len, half, two = rope_cs.shape
-    if two != 2:
-        raise ValueError("rope_cs must be [max_len, rd/2, 2]")
-    _call(fn, dt, x.data_ptr(), xs[0], xs[1], N, H, d, _at(pos, "pos", torch.int32, dev, (N,)),
-          _at(rope_cs, "rope_cs", torch.float32, dev), max_len, 2 * half, layout, out.data_ptr(), os[0], os[1],
-          None if err_flag is None else _at(err_flag, "err_flag", torch.int32, dev),
+    max_len, half, _ = table = rope_cs.shape
+    xs, os = x.stride(), out.stride()
+    if not (out.shape == shape and out.dtype is dtype and x.get_device() == dev and out.get_device() == dev
+            and xs[2] == 1 and os[-1] == 1 and pos.dtype is _I32 and pos.get_device() == dev and pos.shape == (N,)
+            and pos.is_contiguous() and rope_cs.dtype is _F32T and rope_cs.get_device() == dev and table[2] == 2
+            and rope_cs.is_contiguous() and (err_flag is None or _good(err_flag, _I32, dev, err_flag.shape))):
+        _refuse((x, "x", dtype, shape, "last"), (out, "out", dtype, shape, "last"), (pos, "pos", _I32, (N,), None),
+                (rope_cs, "rope_cs", _F32T, (max_len, half, 2), None),
+                (err_flag, "err_flag", _I32, () if err_flag is None else err_flag.shape, None))
+    _call(fn, dt, x.data_ptr(), xs[0], xs[1], N, H, d, pos.data_ptr(), rope_cs.data_ptr(), max_len, 2 * half, layout,
+          out.data_ptr(), os[0], os[1], None if err_flag is None else err_flag.data_ptr(),
           _cuda_stream(dev) if stream is None else stream.cuda_stream)
 
 
@@ -365,47 +364,50 @@ def rope_backward(dout, pos, rope_cs, dx, layout=ROPE_HALF, err_flag=None, strea
     _rope("msa_rope_backward", dout, pos, rope_cs, dx, layout, err_flag, stream)
 
 
-def _cache(Kpages, Vpages, block_table, seq_len, q_off, Hkv, d, dtype, dev):
-    """The batch and cache arguments both paged entry points take, checked: B, the pointer of
-    q_off, K, V and the rest in the order of the C signature."""
-    shape = Kpages.shape
-    if shape[2:] != (Hkv, d):
-        raise ValueError(f"Kpages must be [num_pages, page, {Hkv}, {d}], not {tuple(shape)}")
-    ks = _rows_at(Kpages, "Kpages", dtype, dev, shape)
-    if _rows_at(Vpages, "Vpages", dtype, dev, shape) != ks:
-        raise ValueError("Kpages and Vpages must have the same strides")
-    B, = seq_len.shape
-    max_pages = block_table.shape[-1]
-    return (B, _at(q_off, "q_off", torch.int64, dev, (B + 1,)), Kpages.data_ptr(), Vpages.data_ptr(), shape[0],
-            shape[1], ks[0], ks[1], ks[2], _at(block_table, "block_table", torch.int32, dev, (B, max_pages)),
-            max_pages, _at(seq_len, "seq_len", torch.int32, dev))
-
-
 def paged_append(q, k, v, q_off, seq_len, block_table, Kpages, Vpages, rope_cs=None, q_out=None, pos=None,
                  layout=ROPE_HALF, err_flag=None, stream=None):
     """New tokens into the paged cache (msa_paged_append): k (rotated) and v [N, Hkv, d] into the
     pages [num_pages, page, Hkv, d] (any strides) of their sequences, q (rotated) into q_out.
     q may be None; rope_cs None: no rotation; pos None: cache positions."""
-    dt, dev, dtype = _dt(k), _cuda_dev(), k.dtype
+    dtype, dev = k.dtype, _cuda_dev()
+    dt = _dt(k)
     N, Hkv, d = shape = k.shape
-    ks, vs = _heads_at(k, "k", dtype, dev, shape), _heads_at(v, "v", dtype, dev, shape)
+    cache, B, pages = Kpages.shape, seq_len.shape[0], block_table.shape[-1]
+    ks, vs, ps = k.stride(), v.stride(), Kpages.stride()
+    if not (v.shape == shape and v.dtype is dtype and k.get_device() == dev and v.get_device() == dev
+            and ks[2] == 1 and vs[-1] == 1 and ks[1] == d and vs[1] == d
+            and cache[2:] == (Hkv, d) and Vpages.shape == cache and Kpages.dtype is dtype and Vpages.dtype is dtype
+            and Vpages.stride() == ps and ps[-1] == 1 and Kpages.get_device() == dev and Vpages.get_device() == dev
+            and _good(q_off, _I64, dev, (B + 1,)) and _good(seq_len, _I32, dev, (B,))
+            and _good(block_table, _I32, dev, (B, pages)) and _good(pos, _I32, dev, (N,))
+            and (err_flag is None or _good(err_flag, _I32, dev, err_flag.shape))):
+        _refuse((k, "k", dtype, shape, "heads"), (v, "v", dtype, shape, "heads"),
+                (Kpages, "Kpages", dtype, (*cache[:2], Hkv, d), "last"), (Vpages, "Vpages", dtype, cache, "last"),
+                (q_off, "q_off", _I64, (B + 1,), None), (seq_len, "seq_len", _I32, (B,), None),
+                (block_table, "block_table", _I32, (B, pages), None), (pos, "pos", _I32, (N,), None),
+                (err_flag, "err_flag", _I32, () if err_flag is None else err_flag.shape, None))
+        if Vpages.stride() != ps:
+            raise ValueError("Kpages and Vpages must have the same strides")
     qp = qop = csp = None
     qs = qos = Hq = max_len = half = 0
     if q is not None or q_out is not None:
         if q is None or q_out is None:
             raise ValueError("q and q_out go together")
         Hq = q.shape[1]
-        qs, qos = _heads_at(q, "q", dtype, dev, (N, Hq, d)), _heads_at(q_out, "q_out", dtype, dev, (N, Hq, d))
-        qp, qop = q.data_ptr(), q_out.data_ptr()
+        qs, qos = q.stride(), q_out.stride()
+        if not (q.shape == (N, Hq, d) and q_out.shape == q.shape and q.dtype is dtype and q_out.dtype is dtype
+                and q.get_device() == dev and q_out.get_device() == dev and qs[1:] == (d, 1) and qos[1:] == (d, 1)):
+            _refuse((q, "q", dtype, (N, Hq, d), "heads"), (q_out, "q_out", dtype, (N, Hq, d), "heads"))
+        qs, qos, qp, qop = qs[0], qos[0], q.data_ptr(), q_out.data_ptr()
     if rope_cs is not None:
-        max_len, half, two = rope_cs.shape
-        if two != 2:
-            raise ValueError("rope_cs must be [max_len, rd/2, 2]")
-        csp = _at(rope_cs, "rope_cs", torch.float32, dev)
-    B, qo, *cache = _cache(Kpages, Vpages, block_table, seq_len, q_off, Hkv, d, dtype, dev)
-    _call("msa_paged_append", dt, qp, qs, qop, qos, Hq, k.data_ptr(), ks, v.data_ptr(), vs, N, B, qo, Hkv, d,
-          None if pos is None else _at(pos, "pos", torch.int32, dev, (N,)), csp, max_len, 2 * half, layout, *cache,
-          None if err_flag is None else _at(err_flag, "err_flag", torch.int32, dev),
+        max_len, half, _ = table = rope_cs.shape
+        if not (table[2] == 2 and _good(rope_cs, _F32T, dev, table)):
+            _refuse((rope_cs, "rope_cs", _F32T, (max_len, half, 2), None))
+        csp = rope_cs.data_ptr()
+    _call("msa_paged_append", dt, qp, qs, qop, qos, Hq, k.data_ptr(), ks[0], v.data_ptr(), vs[0], N, B,
+          q_off.data_ptr(), Hkv, d, None if pos is None else pos.data_ptr(), csp, max_len, 2 * half, layout,
+          Kpages.data_ptr(), Vpages.data_ptr(), cache[0], cache[1], ps[0], ps[1], ps[2], block_table.data_ptr(), pages,
+          seq_len.data_ptr(), None if err_flag is None else err_flag.data_ptr(),
           _cuda_stream(dev) if stream is None else stream.cuda_stream)
 
 
@@ -419,22 +421,38 @@ def paged_attn(Q, q_off, max_q, Kpages, Vpages, block_table, seq_len, O, ws, lse
     [N, Hq, d] packed by q_off int64 [B + 1] (at most max_q tokens a sequence), pages
     [num_pages, page, Hkv, d] (any strides), O [N, Hq, d], lse fp32 [Hq, N].  topk_idx int32 [B, k]
     with doc_chunk_off, Kbar and Vbar adds the selected documents' rows (at most Mmax)."""
-    dt, dev, dtype = _dt(Q), _cuda_dev(), Q.dtype
+    dtype, dev = Q.dtype, _cuda_dev()
+    dt = _dt(Q)
     N, Hq, d = shape = Q.shape
-    Hkv = Kpages.shape[2]
-    qs = _heads_at(Q, "Q", dtype, dev, shape)
-    B, qo, *cache = _cache(Kpages, Vpages, block_table, seq_len, q_off, Hkv, d, dtype, dev)
+    cache, B, pages = Kpages.shape, seq_len.shape[0], block_table.shape[-1]
+    Hkv = cache[2]
+    qs, ps = Q.stride(), Kpages.stride()
+    if not (Q.get_device() == dev and qs[2] == 1 and qs[1] == d and Kpages.dtype is dtype and Vpages.dtype is dtype
+            and cache[3] == d and Vpages.shape == cache and Vpages.stride() == ps and ps[-1] == 1
+            and Kpages.get_device() == dev and Vpages.get_device() == dev
+            and _good(q_off, _I64, dev, (B + 1,)) and _good(seq_len, _I32, dev, (B,))
+            and _good(block_table, _I32, dev, (B, pages)) and _good(O, dtype, dev, shape)
+            and _good(lse, _F32T, dev, (Hq, N)) and ws.get_device() == dev and ws.is_contiguous()
+            and (err_flag is None or _good(err_flag, _I32, dev, err_flag.shape))):
+        _refuse((Q, "Q", dtype, shape, "heads"), (Kpages, "Kpages", dtype, (*cache[:3], d), "last"),
+                (Vpages, "Vpages", dtype, cache, "last"), (q_off, "q_off", _I64, (B + 1,), None),
+                (seq_len, "seq_len", _I32, (B,), None), (block_table, "block_table", _I32, (B, pages), None),
+                (O, "O", dtype, shape, None), (lse, "lse", _F32T, (Hq, N), None), (ws, "ws", ws.dtype, ws.shape, None),
+                (err_flag, "err_flag", _I32, () if err_flag is None else err_flag.shape, None))
+        if Vpages.stride() != ps:
+            raise ValueError("Kpages and Vpages must have the same strides")
     idx = off = kb = vb = None
     k = D = C = 0
     if topk_idx is not None:
         if doc_chunk_off is None or Kbar is None or Vbar is None:
             raise ValueError("topk_idx goes with doc_chunk_off, Kbar and Vbar")
         k, D, C = topk_idx.shape[-1], doc_chunk_off.numel() - 1, Kbar.shape[0]
-        idx = _at(topk_idx, "topk_idx", torch.int32, dev, (B, k))
-        off = _at(doc_chunk_off, "doc_chunk_off", torch.int64, dev)
-        kb, vb = _at(Kbar, "Kbar", dtype, dev, (C, Hkv, d)), _at(Vbar, "Vbar", dtype, dev, (C, Hkv, d))
-    _call("msa_paged_attn", dt, Q.data_ptr(), qs, N, B, max_q, qo, Hq, Hkv, d, *cache, idx, k, off, D, C, kb, vb, Mmax,
-          scale, _at(O, "O", dtype, dev, shape),
-          None if lse is None else _at(lse, "lse", torch.float32, dev, (Hq, N)), _at(ws, "ws", ws.dtype, dev),
-          ws.nbytes, None if err_flag is None else _at(err_flag, "err_flag", torch.int32, dev),
+        _refuse((topk_idx, "topk_idx", _I32, (B, k), None), (doc_chunk_off, "doc_chunk_off", _I64, (D + 1,), None),
+                (Kbar, "Kbar", dtype, (C, Hkv, d), None), (Vbar, "Vbar", dtype, (C, Hkv, d), None))
+        idx, off, kb, vb = topk_idx.data_ptr(), doc_chunk_off.data_ptr(), Kbar.data_ptr(), Vbar.data_ptr()
+    _call("msa_paged_attn", dt, Q.data_ptr(), qs[0], N, B, max_q, q_off.data_ptr(), Hq, Hkv, d, Kpages.data_ptr(),
+          Vpages.data_ptr(), cache[0], cache[1], ps[0], ps[1], ps[2], block_table.data_ptr(), pages,
+          seq_len.data_ptr(), idx, k, off, D, C, kb, vb, Mmax, scale, O.data_ptr(),
+          None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.nbytes,
+          None if err_flag is None else err_flag.data_ptr(),
           _cuda_stream(dev) if stream is None else stream.cuda_stream)

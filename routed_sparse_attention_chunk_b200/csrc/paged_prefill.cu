@@ -583,6 +583,18 @@ paged_prefill_kernel(const __grid_constant__ TileMaps maps, PreParams a) {
   }
 }
 
+// setmaxnreg.inc waits for registers that the launch must have brought: were the kernel ever compiled
+// to fewer than the split needs, it would wait forever.  Looked up once per kernel.
+template <int DH>
+cudaError_t registers_cover_split() {
+  static const bool enough = [] {
+    cudaFuncAttributes at;
+    return cudaFuncGetAttributes(&at, paged_prefill_kernel<DH>) == cudaSuccess &&
+           at.numRegs * kThreads >= 256 * kSoftRegs + 128 * kOtherRegs;
+  }();
+  return enough ? cudaSuccess : cudaErrorInvalidConfiguration;
+}
+
 template <int DH>
 cudaError_t prefill_t(const PagedAttnArgs& a, cudaStream_t s) {
   using L = Layout<DH>;
@@ -604,7 +616,9 @@ cudaError_t prefill_t(const PagedAttnArgs& a, cudaStream_t s) {
   d.slots = reinterpret_cast<float*>(reinterpret_cast<char*>(a.part) + marks_bytes(grid));
   d.scale_log2 = a.scale * 1.4426950408889634f;
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(paged_prefill_kernel<DH>, L::kSmem, done);
+  cudaError_t e = registers_cover_split<DH>();
+  if (e != cudaSuccess) return e;
+  e = allow_smem(paged_prefill_kernel<DH>, L::kSmem, done);
   if (e != cudaSuccess) return e;
   count_launch();
   e = launch_pdl(paged_prefill_kernel<DH>, dim3((unsigned)grid), dim3(kThreads), (size_t)L::kSmem, s, maps, d);
