@@ -6,9 +6,10 @@
 // tensor cores (paged_decode.cu, paged_prefill.cu).
 //
 // The fp32 kernel is a single pass over the keys with running row maxima and sums:
-// 256 threads own 16 x RPT query rows (RPT = 1 for a few rows per KV head, 4
-// otherwise), keys come through shared memory 32 at a time, and a thread keeps an
-// RPT x 2 block of scores and an RPT x DH / 16 block of the output in registers.
+// 256 threads own 64 query rows, keys come through shared memory 32 at a time, and a
+// thread keeps a 4 x 2 block of scores and a 4 x DH / 16 block of the output in
+// registers.  Up to 16 rows per KV head stream the keys through registers instead
+// (paged_f32_rows_kernel).
 // All arithmetic is fp32 FMA; scores are compared and subtracted unscaled, so the
 // exponent's argument (s - max) * scale carries only its own rounding.
 #include <math.h>
@@ -30,7 +31,8 @@ constexpr int kSub = 32;  // keys per step of the fp32 kernel
 constexpr int kF32Threads = 256;
 constexpr int kF32ItemCost = 1, kF32Slack = 2;  // see Split
 
-template <int DH, int RPT>
+constexpr int RPT = 4;  // query rows of a thread
+template <int DH>
 struct F32Smem {
   static constexpr int RB = 16 * RPT;
   float Q[RB][DH + 4];
@@ -41,9 +43,9 @@ struct F32Smem {
   Start st;
 };
 
-template <int DH, int RPT>
+template <int DH>
 __global__ void __launch_bounds__(kF32Threads) paged_f32_kernel(PagedAttnArgs a, int TB, Mark* marks, float* slots) {
-  using S = F32Smem<DH, RPT>;
+  using S = F32Smem<DH>;
   constexpr int RB = S::RB, DPT = DH / 16;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   S& sm = *reinterpret_cast<S*>(smem_raw);
@@ -52,14 +54,14 @@ __global__ void __launch_bounds__(kF32Threads) paged_f32_kernel(PagedAttnArgs a,
   const int G = a.Hq / p.Hkv;
   const Split sp{TB, kF32ItemCost, kF32Slack};
   pdl_wait();
-  find_start<RPT == 1>(p, sp, blockIdx.x, gridDim.x, blockIdx.x == 0, &sm.st, reinterpret_cast<ScanScratch*>(sm.row));
+  find_start<false>(p, sp, blockIdx.x, gridDim.x, blockIdx.x == 0, &sm.st, reinterpret_cast<ScanScratch*>(sm.row));
   if (tid == 0) leave_mark(&sm.st, sp, blockIdx.x, marks + blockIdx.x);
   pdl_trigger();
   if (!sm.st.any) return;
   const float sl2 = a.scale * 1.4426950408889634f;
   const float* Q = reinterpret_cast<const float*>(a.Q);
 
-  for (WalkT<RPT == 1> w(sp, &sm.st); w.more(); w.next(p, sp)) {
+  for (WalkT<false> w(sp, &sm.st); w.more(); w.next(p, sp)) {
     const Seq& s = w.s;
     const int tb0 = w.i * TB;
     __syncthreads();  // the previous segment's readers are done
@@ -365,22 +367,238 @@ __global__ void __launch_bounds__(kMergeThreads, 4) merge_kernel(MergeArgs ma) {
   }
 }
 
-// CTAs of the fp32 kernel per SM, by its shared memory and registers.
-int f32_ctas(bool few) { return few ? 4 : 2; }
+// fp32 for up to 16 rows per KV head, bound by HBM: 256 threads stream the tiles' rows straight
+// into registers.  Eight lanes share a key (DH / 8 dimensions each), so a warp takes four keys at
+// once, kAhead times; every group of eight lanes keeps running maxima, sums and outputs of its own
+// for RW rows, merged within the CTA at the segment's end.  With 16 rows (kHalves = 2) half of the
+// warps take rows 0..7, half 8..15.
+template <int DH, int RW, int kHalves>
+struct RowsSmem {
+  static constexpr int kWarps = 8 / kHalves;  // warps that share the keys of a tile
+  float Q[16][DH];
+  float part[8][RW][DH];
+  float2 ml[8][RW];
+  int64_t row[2][kKeys];  // as in F32Smem, of this tile and the next
+  Start st;
+};
 
-template <int DH, int RPT>
-cudaError_t f32_t(const PagedAttnArgs& a, int TB, cudaStream_t s) {
-  using S = F32Smem<DH, RPT>;
-  static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(paged_f32_kernel<DH, RPT>, (int)sizeof(S), done);
+template <int DH, int RW, int kHalves>
+__global__ void __launch_bounds__(kF32Threads, 1) paged_f32_rows_kernel(PagedAttnArgs a, Mark* marks, float* slots) {
+  using S = RowsSmem<DH, RW, kHalves>;
+  constexpr int kVec = DH / 32, kAhead = 2, kPerWarp = kKeys / S::kWarps;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  S& sm = *reinterpret_cast<S*>(smem_raw);
+  const PagedBatch& p = a.p;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, grp = lane >> 3, sub = lane & 7;
+  const int kw = warp % S::kWarps, r0 = warp / S::kWarps * RW;  // this warp's keys and rows
+  const int G = a.Hq / p.Hkv;
+  const Split sp{p.max_q, kF32ItemCost, kF32Slack};
+  pdl_wait();
+  find_start<true>(p, sp, blockIdx.x, gridDim.x, blockIdx.x == 0, &sm.st, reinterpret_cast<ScanScratch*>(sm.row));
+  if (tid == 0) leave_mark(&sm.st, sp, blockIdx.x, marks + blockIdx.x);
+  pdl_trigger();
+  if (!sm.st.any) return;
+  const float sl2 = a.scale * 1.4426950408889634f;
+  const float* Q = reinterpret_cast<const float*>(a.Q);
+  const float minf = -INFINITY;
+
+  for (WalkT<true> w(sp, &sm.st); w.more(); w.next(p, sp)) {
+    const Seq& s = w.s;
+    const int rows = s.nq * G, pos0 = s.len - s.nq;  // rows that exist, position of the first new token
+    // element offset of one key of a tile in its tensor, -1: no key
+    auto locate = [&](int t) -> int64_t {
+      if (t < s.nm) {
+        const int sg = t * kTileSegs + tid / kSegRows, x = tid % kSegRows;
+        if (sg < p.Smax && x < __ldg(a.seg_cnt + w.b * p.Smax + sg))
+          return ((int64_t)(__ldg(a.seg_row + w.b * p.Smax + sg) + x) * p.Hkv + w.g) * DH;
+        return -1;
+      }
+      const int at = (t - s.nm) * kKeys + tid;
+      if (at >= s.len) return -1;
+      const int pi = at / p.page;
+      const int64_t pg = __ldg(p.table + w.b * p.max_pages + pi);
+      if (pg >= 0 && pg < p.num_pages) return pg * a.page_stride + (at - pi * p.page) * a.row_stride + w.g * a.head_stride;
+      raise_flag(p.err_flag, MSA_FLAG_INDEX_OOB);
+      return -1;
+    };
+    __syncthreads();  // the previous segment's readers are done
+    for (int e = tid; e < 16 * (DH / 4); e += kF32Threads) {
+      const int r = e / (DH / 4), c = (e - r * (DH / 4)) * 4, t = r / G;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (t < s.nq) v = __ldg(reinterpret_cast<const float4*>(Q + (s.q0 + t) * a.q_ts + (w.g * G + r % G) * DH + c));
+      *reinterpret_cast<float4*>(&sm.Q[r][c]) = v;
+    }
+    if (tid < kKeys) sm.row[0][tid] = locate(w.t0);
+    float m[RW], l[RW], o[RW][4 * kVec];
+    int last[RW];  // last visible cache position of a row
+#pragma unroll
+    for (int r = 0; r < RW; ++r) {
+      m[r] = minf;
+      l[r] = 0.f;
+      last[r] = r0 + r < rows ? pos0 + (r0 + r) / G : -1;
+#pragma unroll
+      for (int c = 0; c < 4 * kVec; ++c) o[r][c] = 0.f;
+    }
+    for (int t = w.t0; t < w.t0 + w.n; ++t) {
+      const int buf = (t - w.t0) & 1;
+      const bool mem = t < s.nm;
+      __syncthreads();  // this tile's rows are written, the last one's read
+      if (t + 1 < w.t0 + w.n && tid < kKeys) sm.row[buf ^ 1][tid] = locate(t + 1);
+      const float* Ks = reinterpret_cast<const float*>(mem ? a.Kbar : a.K) + sub * 4;
+      const float* Vs = reinterpret_cast<const float*>(mem ? a.Vbar : a.V) + sub * 4;
+      const int base = mem ? 0 : (t - s.nm) * kKeys;
+#pragma unroll 1
+      for (int k0 = kw * kPerWarp; k0 < (kw + 1) * kPerWarp; k0 += 4 * kAhead) {
+        int64_t off[kAhead];
+        float4 kv[kAhead][kVec], vv[kAhead][kVec];
+        bool all = true;  // every row of the warp sees every key of the step
+#pragma unroll
+        for (int n = 0; n < kAhead; ++n) {
+          const int k = k0 + n * 4 + grp;
+          off[n] = sm.row[buf][k];
+          all = all && off[n] >= 0 && (mem || base + k <= pos0);
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) {
+            kv[n][i] = vv[n][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (off[n] >= 0) {
+              kv[n][i] = __ldg(reinterpret_cast<const float4*>(Ks + off[n] + i * 32));
+              vv[n][i] = __ldg(reinterpret_cast<const float4*>(Vs + off[n] + i * 32));
+            }
+          }
+        }
+        all = __all_sync(0xffffffffu, all);
+#pragma unroll
+        for (int r = 0; r < RW; ++r) {
+          float sc[kAhead];
+#pragma unroll
+          for (int n = 0; n < kAhead; ++n) sc[n] = 0.f;
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) {
+            const float4 q = *reinterpret_cast<const float4*>(&sm.Q[r0 + r][sub * 4 + i * 32]);
+#pragma unroll
+            for (int n = 0; n < kAhead; ++n)
+              sc[n] = fmaf(q.x, kv[n][i].x, fmaf(q.y, kv[n][i].y, fmaf(q.z, kv[n][i].z, fmaf(q.w, kv[n][i].w, sc[n]))));
+          }
+          float top = m[r];
+#pragma unroll
+          for (int n = 0; n < kAhead; ++n) {
+#pragma unroll
+            for (int x = 4; x > 0; x >>= 1) sc[n] += __shfl_xor_sync(0xffffffffu, sc[n], x);
+            if (!all && !(off[n] >= 0 && (mem ? r0 + r < rows : base + k0 + n * 4 + grp <= last[r]))) sc[n] = minf;
+            top = fmaxf(top, sc[n]);
+          }
+          const float corr = m[r] == minf ? 0.f : exp2f((m[r] - top) * sl2);
+          m[r] = top;
+          l[r] *= corr;
+#pragma unroll
+          for (int c = 0; c < 4 * kVec; ++c) o[r][c] = corr == 1.f ? o[r][c] : o[r][c] * corr;
+#pragma unroll
+          for (int n = 0; n < kAhead; ++n) {
+            if (!all && sc[n] == minf) continue;  // not seen: whatever V holds stays out
+            const float pw = exp2f((sc[n] - top) * sl2);
+            l[r] += pw;
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) {
+              o[r][4 * i] = fmaf(pw, vv[n][i].x, o[r][4 * i]);
+              o[r][4 * i + 1] = fmaf(pw, vv[n][i].y, o[r][4 * i + 1]);
+              o[r][4 * i + 2] = fmaf(pw, vv[n][i].z, o[r][4 * i + 2]);
+              o[r][4 * i + 3] = fmaf(pw, vv[n][i].w, o[r][4 * i + 3]);
+            }
+          }
+        }
+      }
+    }
+    // the warp's four groups, then the warps; a sum of 0 is a group whose rows saw no key
+#pragma unroll
+    for (int r = 0; r < RW; ++r) {
+#pragma unroll
+      for (int x = 8; x < 32; x <<= 1) {
+        const float mo = __shfl_xor_sync(0xffffffffu, m[r], x), lo = __shfl_xor_sync(0xffffffffu, l[r], x);
+        const float top = fmaxf(m[r], mo);
+        const float f = l[r] == 0.f ? 0.f : exp2f((m[r] - top) * sl2), fo = lo == 0.f ? 0.f : exp2f((mo - top) * sl2);
+        m[r] = top;
+        l[r] = l[r] * f + lo * fo;
+#pragma unroll
+        for (int c = 0; c < 4 * kVec; ++c) {
+          const float y = __shfl_xor_sync(0xffffffffu, o[r][c], x);
+          o[r][c] = (f == 0.f ? 0.f : o[r][c] * f) + (fo == 0.f ? 0.f : y * fo);
+        }
+      }
+      if (grp == 0) {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+          *reinterpret_cast<float4*>(&sm.part[warp][r][sub * 4 + i * 32]) =
+              make_float4(o[r][4 * i], o[r][4 * i + 1], o[r][4 * i + 2], o[r][4 * i + 3]);
+        if (sub == 0) sm.ml[warp][r] = make_float2(m[r], l[r]);
+      }
+    }
+    __syncthreads();
+    const bool whole = w.whole();
+    float* slot = slots + slot_of(blockIdx.x, w.f, sm.st.f0) * slot_floats(16, DH);
+    for (int e = tid; e < rows * (DH / 4); e += kF32Threads) {
+      const int r = e / (DH / 4), c = (e - r * (DH / 4)) * 4, w0 = r / RW * S::kWarps;
+      float top = minf, sum = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int x = 0; x < S::kWarps; ++x) top = fmaxf(top, sm.ml[w0 + x][r % RW].x);
+#pragma unroll
+      for (int x = 0; x < S::kWarps; ++x) {
+        const float2 ml = sm.ml[w0 + x][r % RW];
+        if (ml.y == 0.f) continue;
+        const float f = exp2f((ml.x - top) * sl2);
+        const float4 v = *reinterpret_cast<const float4*>(&sm.part[w0 + x][r % RW][c]);
+        sum += ml.y * f;
+        acc.x = fmaf(v.x, f, acc.x);
+        acc.y = fmaf(v.y, f, acc.y);
+        acc.z = fmaf(v.z, f, acc.z);
+        acc.w = fmaf(v.w, f, acc.w);
+      }
+      const int t = r / G, h = w.g * G + r % G;
+      if (whole) {
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.O) + ((s.q0 + t) * a.Hq + h) * DH + c) =
+            make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        if (a.lse && c == 0)
+          a.lse[(int64_t)h * p.N + s.q0 + t] = sum == 0.f ? minf : top * a.scale + logf(sum);
+      } else {
+        *reinterpret_cast<float4*>(slot + r * DH + c) = acc;
+        if (c == 0) *reinterpret_cast<float2*>(slot + 16 * DH + 2 * r) = make_float2(top, sum);
+      }
+    }
+  }
+}
+
+// CTAs of the fp32 kernels per SM, by their registers and shared memory.
+int f32_ctas(bool few) { return few ? 1 : 2; }
+
+template <typename Kernel, typename... Args>
+cudaError_t f32_launch(Kernel kernel, size_t smem, std::atomic<uint64_t>& done, int grid, int rows,
+                       const PagedAttnArgs& a, cudaStream_t s, Args... args) {
+  cudaError_t e = allow_smem(kernel, (int)smem, done);
   if (e != cudaSuccess) return e;
-  const int grid = f32_ctas(RPT == 1) * sm_count();
   Mark* marks = reinterpret_cast<Mark*>(a.part);
   float* slots = reinterpret_cast<float*>(reinterpret_cast<char*>(a.part) + marks_bytes(grid));
   count_launch();
-  e = launch_pdl(paged_f32_kernel<DH, RPT>, dim3((unsigned)grid), dim3(kF32Threads), sizeof(S), s, a, TB, marks, slots);
+  e = launch_pdl(kernel, dim3((unsigned)grid), dim3(kF32Threads), smem, s, a, args..., marks, slots);
   if (e != cudaSuccess) return e;
-  return launch_merge(MSA_F32, false, MergeArgs{a, marks, slots, grid, S::RB, a.scale * 1.4426950408889634f}, s);
+  return launch_merge(MSA_F32, false, MergeArgs{a, marks, slots, grid, rows, a.scale * 1.4426950408889634f}, s);
+}
+template <int DH>
+cudaError_t f32_block(const PagedAttnArgs& a, cudaStream_t s) {
+  static std::atomic<uint64_t> done{0};
+  return f32_launch(paged_f32_kernel<DH>, sizeof(F32Smem<DH>), done, f32_ctas(false) * sm_count(), F32Smem<DH>::RB, a, s,
+                    F32Smem<DH>::RB / (a.Hq / a.p.Hkv));
+}
+template <int DH, int RW, int kHalves>
+cudaError_t f32_rows(const PagedAttnArgs& a, cudaStream_t s) {
+  static std::atomic<uint64_t> done{0};
+  return f32_launch(paged_f32_rows_kernel<DH, RW, kHalves>, sizeof(RowsSmem<DH, RW, kHalves>), done,
+                    f32_ctas(true) * sm_count(), 16, a, s);
+}
+template <int DH>
+cudaError_t f32_few(const PagedAttnArgs& a, cudaStream_t s) {
+  const int R = a.Hq / a.p.Hkv * a.p.max_q;
+  return R <= 4 ? f32_rows<DH, 4, 1>(a, s) : R <= 8 ? f32_rows<DH, 8, 1>(a, s) : f32_rows<DH, 8, 2>(a, s);
 }
 
 // Few rows per KV head: the kernels that hold at most 16 of them.
@@ -410,9 +628,8 @@ size_t paged_attn_partial_bytes(msa_dtype dt, int Hq, int Hkv, int d, int max_q)
 cudaError_t launch_paged_attn(msa_dtype dt, const PagedAttnArgs& a, cudaStream_t s) {
   const bool few = paged::few_rows(a.Hq, a.p.Hkv, a.p.max_q);
   if (dt == MSA_F32) {
-    const int TB = few ? a.p.max_q : 64 / (a.Hq / a.p.Hkv);
-    if (a.d == 64) return few ? paged::f32_t<64, 1>(a, TB, s) : paged::f32_t<64, 4>(a, TB, s);
-    return few ? paged::f32_t<128, 1>(a, TB, s) : paged::f32_t<128, 4>(a, TB, s);
+    if (a.d == 64) return few ? paged::f32_few<64>(a, s) : paged::f32_block<64>(a, s);
+    return few ? paged::f32_few<128>(a, s) : paged::f32_block<128>(a, s);
   }
   return few && a.d == 128 ? launch_paged_decode(a, s) : launch_paged_prefill(a, s);
 }
