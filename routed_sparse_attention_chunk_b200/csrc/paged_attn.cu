@@ -385,7 +385,7 @@ struct RowsSmem {
 template <int DH, int RW, int kHalves>
 __global__ void __launch_bounds__(kF32Threads, 1) paged_f32_rows_kernel(PagedAttnArgs a, Mark* marks, float* slots) {
   using S = RowsSmem<DH, RW, kHalves>;
-  constexpr int kVec = DH / 32, kAhead = 2, kPerWarp = kKeys / S::kWarps;
+  constexpr int kVec = DH / 32, kAhead = RW == 4 ? 4 : 2, kPerWarp = kKeys / S::kWarps;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   S& sm = *reinterpret_cast<S*>(smem_raw);
   const PagedBatch& p = a.p;
@@ -609,7 +609,7 @@ bool few_rows(int Hq, int Hkv, int max_q) { return (int64_t)(Hq / Hkv) * max_q <
 cudaError_t launch_merge(msa_dtype dt, bool quads, const MergeArgs& m, cudaStream_t s) {
   const int d = m.a.d;
   auto k = dt == MSA_F32 ? (d == 64 ? merge_kernel<float, 64, false> : merge_kernel<float, 128, false>)
-           : !quads      ? merge_kernel<__nv_bfloat16, 128, false>
+           : !quads      ? (d == 64 ? merge_kernel<__nv_bfloat16, 64, false> : merge_kernel<__nv_bfloat16, 128, false>)
                          : (d == 64 ? merge_kernel<__nv_bfloat16, 64, true> : merge_kernel<__nv_bfloat16, 128, true>);
   const dim3 grid((unsigned)(m.grid - 1), (unsigned)((m.rows + kMergeRows - 1) / kMergeRows));
   count_launch();
@@ -621,7 +621,7 @@ cudaError_t launch_merge(msa_dtype dt, bool quads, const MergeArgs& m, cudaStrea
 size_t paged_attn_partial_bytes(msa_dtype dt, int Hq, int Hkv, int d, int max_q) {
   const bool few = paged::few_rows(Hq, Hkv, max_q);
   const int grid = dt == MSA_F32 ? paged::f32_ctas(few) * sm_count() : sm_count();
-  const int rows = dt == MSA_F32 ? (few ? 16 : 64) : (few && d == 128 ? Hq / Hkv * max_q : 128);
+  const int rows = dt == MSA_F32 ? (few ? 16 : 64) : (few ? Hq / Hkv * max_q : 128);
   return paged::marks_bytes(grid) + 2 * (size_t)grid * paged::slot_floats(rows, d) * sizeof(float);
 }
 
@@ -631,7 +631,7 @@ cudaError_t launch_paged_attn(msa_dtype dt, const PagedAttnArgs& a, cudaStream_t
     if (a.d == 64) return few ? paged::f32_few<64>(a, s) : paged::f32_block<64>(a, s);
     return few ? paged::f32_few<128>(a, s) : paged::f32_block<128>(a, s);
   }
-  return few && a.d == 128 ? launch_paged_decode(a, s) : launch_paged_prefill(a, s);
+  return few ? launch_paged_decode(a, s) : launch_paged_prefill(a, s);
 }
 
 }  // namespace msa

@@ -1,6 +1,6 @@
 // Attention over a paged cache for a few query rows per KV head (paged_attn.cu):
 // the R = G * max_q <= 16 rows of one sequence and KV head against
-// [selected memory rows ++ cached tokens], bf16, d = 128.
+// [selected memory rows ++ cached tokens], bf16.
 //
 // Every K and V row is read once and used for at most 16 dot products, so the
 // kernel is shaped for HBM bandwidth; the contractions run on the tensor cores
@@ -36,9 +36,7 @@ namespace {
 using namespace sm100;
 using namespace paged;
 
-constexpr int kDH = 128;
 constexpr int kMaxRows = 16;            // R = G * Tq (the MMA's N, padded to 16)
-constexpr int kStages = 3;
 constexpr int kThreads = 192;
 constexpr int kItemCost = 2, kSlack = 0;  // see Split
 constexpr uint32_t kWaitPolls = 1u << 24;
@@ -62,13 +60,16 @@ struct DecParams {
   float scale_log2;
 };
 
+template <int DH>
 struct DLayout {
-  static constexpr int kTile = Tile<kDH>::kBytes;     // one K (or V) tile
+  static constexpr int kStages = DH == 64 ? 6 : 3;    // of K and V: 192 KB in flight either way
+  static constexpr int kTile = Tile<DH>::kBytes;     // one K (or V) tile
   static constexpr int kStage = 2 * kTile;
-  static constexpr int kQ = kMaxRows * kDH * 2;       // Q rows, K-major, 128-byte swizzle (two buffers)
+  static constexpr int kQ = kMaxRows * DH * 2;        // Q rows, K-major, 128-byte swizzle (two buffers)
   static constexpr int kP = kMaxRows * kKeys * 2;     // P^T rows (query rows x keys); two buffers
   static constexpr int kRed = 2 * kMaxRows * 4 * 4;    // [maxima, sums][rows][4 warps]
-  static constexpr int kSmem = 1024 + kStages * kStage + 2 * kQ + 2 * kP + kRed + 8 * 19 + (int)sizeof(Start);
+  static constexpr int kBars = 2 * kStages + 13;       // and tensor memory's address, the stop flag, the odd flag
+  static constexpr int kSmem = 1024 + kStages * kStage + 2 * kQ + 2 * kP + kRed + 8 * kBars + (int)sizeof(Start);
   static_assert(kSmem <= 232448, "shared memory of one CTA");
   static constexpr uint32_t kTmemCols = 64;           // S0, S1, O (16 columns each)
 };
@@ -105,28 +106,30 @@ __device__ __forceinline__ int sw128_off(int row, int col, int rows) {
 
 // kR >= R is the number of query rows the softmax threads handle (4, 8 or 16);
 // the MMA's N stays 16 and the columns past kR are never read.
-template <int kR>
+template <int DH, int kR>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_decode_kernel(const __grid_constant__ TileMaps maps, DecParams a) {
+  using L = DLayout<DH>;
+  constexpr int kStages = L::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* ring = smem;
-  uint8_t* Qs = ring + kStages * DLayout::kStage;  // two buffers, alternating by segment
-  uint8_t* Ps = Qs + 2 * DLayout::kQ;
-  float* red_s = reinterpret_cast<float*>(Ps + 2 * DLayout::kP);  // [2][16 rows][4 warps]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(red_s) + DLayout::kRed);
-  uint64_t* kv_full = bars;            // [3]
-  uint64_t* kv_empty = bars + 3;       // [3]
-  uint64_t* s_full = bars + 6;         // [2]
-  uint64_t* s_free = bars + 8;         // [2]
-  uint64_t* q_ready = bars + 10;
-  uint64_t* p_full = bars + 11;        // [2] per P buffer
-  uint64_t* o_done = bars + 13;        // [2] per P buffer: its P V has completed
-  uint64_t* drain = bars + 15;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 16);
-  volatile int* abort_s = reinterpret_cast<volatile int*>(bars + 17);
+  uint8_t* Qs = ring + kStages * L::kStage;  // two buffers, alternating by segment
+  uint8_t* Ps = Qs + 2 * L::kQ;
+  float* red_s = reinterpret_cast<float*>(Ps + 2 * L::kP);  // [2][16 rows][4 warps]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(red_s) + L::kRed);
+  uint64_t* kv_full = bars;                  // [kStages]
+  uint64_t* kv_empty = kv_full + kStages;    // [kStages]
+  uint64_t* s_full = kv_empty + kStages;     // [2]
+  uint64_t* s_free = s_full + 2;             // [2]
+  uint64_t* q_ready = s_free + 2;
+  uint64_t* p_full = q_ready + 1;            // [2] per P buffer
+  uint64_t* o_done = p_full + 2;             // [2] per P buffer: its P V has completed
+  uint64_t* drain = o_done + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_s = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* odd_s = abort_s + 1;  // a value that is not finite (row_not_finite)
-  Start* start = reinterpret_cast<Start*>(bars + 19);
+  Start* start = reinterpret_cast<Start*>(bars + L::kBars);
 
   const PagedBatch& p = a.p;
   const Split sp{p.max_q, kItemCost, kSlack};  // one block of tokens per sequence
@@ -160,7 +163,7 @@ paged_decode_kernel(const __grid_constant__ TileMaps maps, DecParams a) {
     return;
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, DLayout::kTmemCols);
+    tmem_alloc(tmem_slot, L::kTmemCols);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -192,16 +195,16 @@ paged_decode_kernel(const __grid_constant__ TileMaps maps, DecParams a) {
         int ok = 1;
         if (lane == 0) {
           ok = mbar_wait_or_stop(&kv_empty[st], ((it / kStages) & 1) ^ 1, kWaitPolls, abort_s);
-          if (ok) mbar_arrive_expect_tx(&kv_full[st], (uint32_t)(boxes * rows * kDH * 2 * 2));
+          if (ok) mbar_arrive_expect_tx(&kv_full[st], (uint32_t)(boxes * rows * DH * 2 * 2));
         }
         if (!__shfl_sync(0xffffffffu, ok, 0)) {
           stop = true;
           break;
         }
         if (x.mine) {
-          uint8_t* Kd = ring + st * DLayout::kStage;
-          load_box<kDH>(Kd, &maps.k, &maps.kbar, a.pm, mem, x, w.g, lane, &kv_full[st]);
-          load_box<kDH>(Kd + DLayout::kTile, &maps.v, &maps.vbar, a.pm, mem, x, w.g, lane, &kv_full[st]);
+          uint8_t* Kd = ring + st * L::kStage;
+          load_box<DH>(Kd, &maps.k, &maps.kbar, a.pm, mem, x, w.g, lane, &kv_full[st]);
+          load_box<DH>(Kd + L::kTile, &maps.v, &maps.vbar, a.pm, mem, x, w.g, lane, &kv_full[st]);
         }
         x = nx;
       }
@@ -218,12 +221,12 @@ paged_decode_kernel(const __grid_constant__ TileMaps maps, DecParams a) {
     // ---------------------------------------------------------------- MMA issuer
     if (lane == 0) {
       constexpr uint32_t idS = idesc_bf16_f32(kKeys, kMaxRows);                              // K x Q^T
-      constexpr uint32_t idO = idesc_bf16_f32(kDH, kMaxRows, /*b_mn=*/false, /*a_mn=*/true);  // V^T x P^T
+      constexpr uint32_t idO = idesc_bf16_f32(DH, kMaxRows, /*b_mn=*/false, /*a_mn=*/true);  // V^T x P^T
       const uint32_t p0 = smem_u32(Ps);
       uint32_t it = 0, nseg = 0;  // it: tiles (K/V stages, S and P buffers); nseg: segments
       for (Walk w(sp, start); w.more() && !*abort_s; w.next(p, sp), ++nseg) {
         const int T = w.n;
-        const uint32_t q0 = smem_u32(Qs + (nseg & 1) * DLayout::kQ);
+        const uint32_t q0 = smem_u32(Qs + (nseg & 1) * L::kQ);
         if (!mbar_wait_or_stop(q_ready, nseg & 1, kWaitPolls, abort_s)) break;
         // Issue S = K Q^T of a tile as soon as its K/V stage and an S buffer are
         // ready, and O += V^T P^T of a tile as soon as its P is: one thread polls
@@ -237,11 +240,11 @@ paged_decode_kernel(const __grid_constant__ TileMaps maps, DecParams a) {
             const uint32_t g = it + nS, st = g % kStages, round = g / kStages, sb = g & 1;
             if (mbar_test(&kv_full[st], round & 1) && mbar_test(&s_free[sb], ((g >> 1) & 1) ^ 1)) {
               tc_fence_after();
-              const uint32_t k0 = smem_u32(ring + st * DLayout::kStage);
+              const uint32_t k0 = smem_u32(ring + st * L::kStage);
 #pragma unroll
-              for (int k = 0; k < kDH / 16; ++k) {
+              for (int k = 0; k < DH / 16; ++k) {
                 const int box = k >> 2, kk = k & 3;
-                mma_bf16_ss(tS + sb * 16, desc_k_sw128_sbo(k0 + box * 1024 + kk * 32, Tile<kDH>::kGroup),
+                mma_bf16_ss(tS + sb * 16, desc_k_sw128_sbo(k0 + box * 1024 + kk * 32, Tile<DH>::kGroup),
                             desc_k_sw128(q0 + box * (kMaxRows * 128) + kk * 32), idS, k > 0 ? 1u : 0u);
               }
               mma_commit(&s_full[sb]);
@@ -253,12 +256,12 @@ paged_decode_kernel(const __grid_constant__ TileMaps maps, DecParams a) {
             const uint32_t g = it + nP, st = g % kStages, pb = g & 1;
             if (mbar_test(&p_full[pb], (g >> 1) & 1)) {
               tc_fence_after();
-              const uint32_t v0 = smem_u32(ring + st * DLayout::kStage + DLayout::kTile);
-              const uint32_t pp = p0 + pb * DLayout::kP;
+              const uint32_t v0 = smem_u32(ring + st * L::kStage + L::kTile);
+              const uint32_t pp = p0 + pb * L::kP;
 #pragma unroll
               for (int k = 0; k < kKeys / 16; ++k) {
                 const int box = k >> 2, kk = k & 3;
-                mma_bf16_ss(tO, desc_mn_sw128_sbo(v0 + k * 2 * Tile<kDH>::kGroup, 1024, Tile<kDH>::kGroup),
+                mma_bf16_ss(tO, desc_mn_sw128_sbo(v0 + k * 2 * Tile<DH>::kGroup, 1024, Tile<DH>::kGroup),
                             desc_k_sw128(pp + box * (kMaxRows * 128) + kk * 32), idO, (nP > 0 || k > 0) ? 1u : 0u);
               }
               mma_commit(&o_done[pb]);
@@ -278,31 +281,35 @@ paged_decode_kernel(const __grid_constant__ TileMaps maps, DecParams a) {
   } else {
     // ---------------------------------------------------------------- softmax / output
     const int q = warp & 3;
-    const int r_lane = q * 32 + lane;               // this thread's TMEM lane: key of S^T, dim of O^T
+    const int r_lane = q * 32 + lane;               // this thread's TMEM lane: key of S^T
     const uint32_t lane_off = (uint32_t)(q * 32) << 16;
+    // this thread's dimension of O^T: a product of M = 64 leaves its rows in the first 16 lanes of
+    // each warp's 32
+    const int dim = DH == 128 ? r_lane : (lane < 16 ? q * 16 + lane : -1);
     const int et = tid - 64;                        // 0..127
-    // Q rows of a segment into a swizzled K-major buffer: element i of R * 16
-    // 16-byte pieces is row r = i / 16 (token r / G, head g * G + r % G); rows of
-    // tokens the sequence does not have are zeros.
-    auto load_q = [&](const Walk& w, uint4 (&v)[2]) {
+    // Q rows of a segment into a swizzled K-major buffer: 16-byte piece i of 16 rows is row
+    // r = i / (DH / 8) (token r / G, head g * G + r % G); rows of tokens the sequence does not have
+    // are zeros.
+    constexpr int kPieces = DH / 8, kEach = kMaxRows * kPieces / 128;
+    auto load_q = [&](const Walk& w, uint4 (&v)[kEach]) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int i = et + 128 * k, r = i >> 4, c8 = (i & 15) * 8;
+      for (int k = 0; k < kEach; ++k) {
+        const int i = et + 128 * k, r = i / kPieces, c8 = (i % kPieces) * 8;
         v[k] = make_uint4(0, 0, 0, 0);
         const int t = r / a.G, h = w.g * a.G + r % a.G;
-        if (t < w.s.nq) v[k] = __ldg(reinterpret_cast<const uint4*>(a.Q + (w.s.q0 + t) * a.q_ts + h * kDH + c8));
+        if (t < w.s.nq) v[k] = __ldg(reinterpret_cast<const uint4*>(a.Q + (w.s.q0 + t) * a.q_ts + h * DH + c8));
       }
     };
-    auto store_q = [&](uint8_t* buf, const uint4 (&v)[2]) {
+    auto store_q = [&](uint8_t* buf, const uint4 (&v)[kEach]) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int i = et + 128 * k, r = i >> 4, c8 = (i & 15) * 8;
+      for (int k = 0; k < kEach; ++k) {
+        const int i = et + 128 * k, r = i / kPieces, c8 = (i % kPieces) * 8;
         *reinterpret_cast<uint4*>(buf + sw128_off(r, c8, kMaxRows)) = v[k];
       }
     };
     Walk w(sp, start);
     {
-      uint4 v[2];
+      uint4 v[kEach];
       load_q(w, v);
       store_q(Qs, v);
     }
@@ -322,7 +329,7 @@ paged_decode_kernel(const __grid_constant__ TileMaps maps, DecParams a) {
       Walk wn = w;
       wn.next(p, sp);
       const bool more = wn.more();
-      uint4 qn[2];
+      uint4 qn[kEach];
       if (more) load_q(wn, qn);
       const int T = w.n, rows = w.s.nq * a.G;  // rows < kR that exist
       const int pos0 = w.s.len - w.s.nq;       // position of the first new token
@@ -357,9 +364,9 @@ paged_decode_kernel(const __grid_constant__ TileMaps maps, DecParams a) {
         // has landed (S read the same barrier's K); this wait makes it visible here.
         if (mem ? __any_sync(0xffffffffu, low > 0) : key - r_lane + kKeys - 1 > pos0) {
           hold(&kv_full[g % kStages], (g / kStages) & 1);
-          uint8_t* vt = ring + (g % kStages) * DLayout::kStage + DLayout::kTile;
-          if (mem ? low > 0 : key >= w.s.len) zero_row<kDH>(vt, r_lane);
-          else if (!mem && key > pos0 && row_not_finite<kDH>(vt, r_lane)) *odd_s = 1;
+          uint8_t* vt = ring + (g % kStages) * L::kStage + L::kTile;
+          if (mem ? low > 0 : key >= w.s.len) zero_row<DH>(vt, r_lane);
+          else if (!mem && key > pos0 && row_not_finite<DH>(vt, r_lane)) *odd_s = 1;
           __syncwarp();
         }
         // The maximum moves only where a score passes it by 2^8 (always in the first tile with a
@@ -414,11 +421,11 @@ paged_decode_kernel(const __grid_constant__ TileMaps maps, DecParams a) {
         }
 #pragma unroll
         for (int r = 0; r < kR; ++r)
-          *reinterpret_cast<__nv_bfloat16*>(Ps + (g & 1) * DLayout::kP + sw128_off(r, r_lane, kMaxRows)) =
+          *reinterpret_cast<__nv_bfloat16*>(Ps + (g & 1) * L::kP + sw128_off(r, r_lane, kMaxRows)) =
               __float2bfloat16_rn(pr[r]);
         // The other Q buffer was last read by the previous segment's S MMAs,
         // all complete before that segment's last P V.
-        if (j == 0 && more) store_q(Qs + ((nseg + 1) & 1) * DLayout::kQ, qn);
+        if (j == 0 && more) store_q(Qs + ((nseg + 1) & 1) * L::kQ, qn);
         fence_async_smem();
         tc_fence_before();
         mbar_arrive(&p_full[g & 1]);
@@ -443,7 +450,7 @@ paged_decode_kernel(const __grid_constant__ TileMaps maps, DecParams a) {
       }
       bar_softmax();
       const bool whole = w.whole();
-      float* slot = a.slots + slot_of(blockIdx.x, w.f, start->f0) * slot_floats(a.R, kDH);
+      float* slot = a.slots + slot_of(blockIdx.x, w.f, start->f0) * slot_floats(a.R, DH);
       int t = 0, hh = 0;  // row r's token and head of the group
 #pragma unroll
       for (int r = 0; r < kR; ++r) {
@@ -454,13 +461,13 @@ paged_decode_kernel(const __grid_constant__ TileMaps maps, DecParams a) {
           // a sum of 0: no key was visible
           const float inv = l == 0.f ? 0.f : 1.f / l;
           const int h = w.g * a.G + hh;
-          a.O[((w.s.q0 + t) * a.Hq + h) * kDH + r_lane] = __float2bfloat16_rn(l == 0.f ? 0.f : o[r] * inv);
+          if (dim >= 0) a.O[((w.s.q0 + t) * a.Hq + h) * DH + dim] = __float2bfloat16_rn(l == 0.f ? 0.f : o[r] * inv);
           if (a.lse && et == 0)
             a.lse[(int64_t)h * p.N + w.s.q0 + t] =
                 l == 0.f ? -INFINITY : (m_run[r] + log2f(l)) * 0.69314718055994531f;
         } else {
-          slot[r * kDH + r_lane] = o[r];
-          if (et == 0) *reinterpret_cast<float2*>(slot + a.R * kDH + 2 * r) = make_float2(m_run[r], l);
+          if (dim >= 0) slot[r * DH + dim] = o[r];
+          if (et == 0) *reinterpret_cast<float2*>(slot + a.R * DH + 2 * r) = make_float2(m_run[r], l);
         }
         if (++hh == a.G) {
           hh = 0;
@@ -478,7 +485,7 @@ paged_decode_kernel(const __grid_constant__ TileMaps maps, DecParams a) {
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, DLayout::kTmemCols);
+    tmem_dealloc(tmem, L::kTmemCols);
   }
   if (tid == 0) {
     if (*abort_s) raise_flag(p.err_flag, MSA_FLAG_TIMEOUT);
@@ -486,12 +493,12 @@ paged_decode_kernel(const __grid_constant__ TileMaps maps, DecParams a) {
   }
 }
 
-}  // namespace
-
-cudaError_t launch_paged_decode(const PagedAttnArgs& a, cudaStream_t s) {
+template <int DH>
+cudaError_t decode_t(const PagedAttnArgs& a, cudaStream_t s) {
+  using L = DLayout<DH>;
   TileMaps maps;
   DecParams d;
-  if (!make_tile_maps<kDH>(a, &maps, &d.pm)) return cudaErrorInvalidValue;
+  if (!make_tile_maps<DH>(a, &maps, &d.pm)) return cudaErrorInvalidValue;
   const int grid = sm_count(), G = a.Hq / a.p.Hkv;
   d.p = a.p;
   d.Q = reinterpret_cast<const __nv_bfloat16*>(a.Q);
@@ -506,14 +513,22 @@ cudaError_t launch_paged_decode(const PagedAttnArgs& a, cudaStream_t s) {
   d.marks = reinterpret_cast<Mark*>(a.part);
   d.slots = reinterpret_cast<float*>(reinterpret_cast<char*>(a.part) + marks_bytes(grid));
   d.scale_log2 = a.scale * 1.4426950408889634f;
-  auto kern = d.R <= 4 ? paged_decode_kernel<4> : (d.R <= 8 ? paged_decode_kernel<8> : paged_decode_kernel<16>);
+  auto kern = d.R <= 4   ? paged_decode_kernel<DH, 4>
+              : d.R <= 8 ? paged_decode_kernel<DH, 8>
+                         : paged_decode_kernel<DH, 16>;
   static std::atomic<uint64_t> done[3];
-  cudaError_t e = allow_smem(kern, DLayout::kSmem, done[d.R <= 4 ? 0 : (d.R <= 8 ? 1 : 2)]);
+  cudaError_t e = allow_smem(kern, L::kSmem, done[d.R <= 4 ? 0 : (d.R <= 8 ? 1 : 2)]);
   if (e != cudaSuccess) return e;
   count_launch();
-  e = launch_pdl(kern, dim3((unsigned)grid), dim3(kThreads), (size_t)DLayout::kSmem, s, maps, d);
+  e = launch_pdl(kern, dim3((unsigned)grid), dim3(kThreads), (size_t)L::kSmem, s, maps, d);
   if (e != cudaSuccess) return e;
   return launch_merge(MSA_BF16, false, MergeArgs{a, d.marks, d.slots, grid, d.R, 1.f}, s);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_decode(const PagedAttnArgs& a, cudaStream_t s) {
+  return a.d == 64 ? decode_t<64>(a, s) : decode_t<128>(a, s);
 }
 
 }  // namespace msa
