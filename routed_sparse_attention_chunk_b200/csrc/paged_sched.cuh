@@ -118,7 +118,8 @@ __device__ __forceinline__ void find_start(const PagedBatch& p, const Split& sp,
   const int chunk = (int)(((uint32_t)p.B + nt - 1) / (uint32_t)nt);  // B < 2^31
   const int64_t b0 = min(p.B, (int64_t)tid * chunk), b1 = min(p.B, b0 + chunk);
   int64_t mine = 0;         // units of this thread's sequences
-  int items = 0, most = 0;  // their blocks (at most N < 2^31), the tiles of the largest
+  int items = 0, most = 0;  // their blocks (no count above 2^20 is needed, and offsets out of order could
+                            // bring more than 32 bits hold), the tiles of the largest
   int64_t per = 1, f0 = 0, rest = 0, b = b0;
   bool one = false, any = false, owner = false;
   int g = 0;
@@ -133,7 +134,7 @@ __device__ __forceinline__ void find_start(const PagedBatch& p, const Split& sp,
       const int64_t units = (kOneBlock ? 0 : tiles_before(s, TB, nb - 1)) + last + (int64_t)nb * sp.cost;
       if (pass == 0) {
         mine += units;
-        items += nb;
+        items = (int)min((uint32_t)items + (uint32_t)nb, 1u << 20);
         most = max(most, last);
       } else {
         const int64_t n = one ? nb : units;
