@@ -5,18 +5,19 @@
 // by the work split (paged_sched.cuh) and the fp32 kernel; bf16 runs on the
 // tensor cores (paged_decode.cu, paged_prefill.cu).
 //
-// The fp32 kernel is a single pass over the keys with running row maxima and sums:
-// 256 threads own 64 query rows, keys come through shared memory 32 at a time, and a
-// thread keeps a 4 x 2 block of scores and a 4 x DH / 16 block of the output in
-// registers.  Up to 16 rows per KV head stream the keys through registers instead
-// (paged_f32_rows_kernel).
-// All arithmetic is fp32 FMA; scores are compared and subtracted unscaled, so the
+// The fp32 kernels are a single pass over the keys with running row maxima and sums:
+// blocks of 32 or 64 query rows over tiles of keys in shared memory
+// (paged_f32_kernel), and up to 16 rows per KV head with the keys streamed through
+// registers (paged_f32_rows_kernel).  All arithmetic is fp32 FMA; scores are compared and subtracted unscaled, so the
 // exponent's argument (s - max) * scale carries only its own rounding.
 #include <math.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
 #include "paged_sched.cuh"
+#include "sm100.cuh"
 #include "tma_host.h"
 
 namespace msa {
@@ -27,30 +28,51 @@ cudaError_t launch_paged_prefill(const PagedAttnArgs& a, cudaStream_t s);
 namespace paged {
 namespace {
 
-constexpr int kSub = 32;  // keys per step of the fp32 kernel
+using namespace sm100;
+
 constexpr int kF32Threads = 256;
 constexpr int kF32ItemCost = 1, kF32Slack = 2;  // see Split
 
-constexpr int RPT = 4;  // query rows of a thread
-template <int DH>
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool have) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(have ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// The block kernel.  RG groups of 16 query rows times 8 / RG parts of a tile's 128 keys, a warp
+// each: a thread keeps a 4 x 4 block of scores per 32 keys (rows ty + 4 j, keys tx + 8 i; 8 shared
+// memory wavefronts per 64 FMA instructions) and 4 x DH / 8 values of the output.  Every warp has
+// running maxima and sums of its own over its keys, merged at the segment's end, so its weights
+// never leave it.  K of the next tile is copied while P V runs, V while Q K^T does.  Bound by FMA
+// issue and shared memory together: two values an instruction (f32x2), and no question about a key
+// per FMA where the warp sees its whole part, took 1,050 tokens x 32 heads over 2,200 keys from 1,231
+// to 887 us, 43 TFLOP/s; blocks of 64 rows x 32 keys with 4 x 2 scores a thread had taken 1,127.
+template <int DH, int RG>
 struct F32Smem {
-  static constexpr int RB = 16 * RPT;
+  static constexpr int RB = 16 * RG;              // query rows
+  static constexpr int kParts = 8 / RG;           // warps that share a tile's keys
+  static constexpr int kPerWarp = kKeys / kParts;
+  static constexpr int kCtas = DH == 64 && RG == 2 ? 2 : 1;  // per SM, by registers and shared memory
   float Q[RB][DH + 4];
-  float K[kSub][DH + 4];
-  float V[kSub][DH + 4];
-  float P[RB][kSub + 4];
-  int64_t row[kKeys];  // element offset of each key of the tile in its tensor, -1: no key
+  float K[kKeys][DH + 4];  // at a segment's end the outputs of the parts
+  float V[kKeys][DH + 4];
+  float P[8][16][kPerWarp + 8];
+  float2 ml[kParts][RB];   // row maxima and sums of the parts
+  int64_t row[2][kKeys];   // element offset of each key of this tile and the next in its tensor, -1: no key
   Start st;
+  static_assert(kParts * RB * DH <= kKeys * (DH + 4), "the outputs of the parts");
 };
 
-template <int DH>
-__global__ void __launch_bounds__(kF32Threads) paged_f32_kernel(PagedAttnArgs a, int TB, Mark* marks, float* slots) {
-  using S = F32Smem<DH>;
-  constexpr int RB = S::RB, DPT = DH / 16;
+template <int DH, int RG>
+__global__ void __launch_bounds__(kF32Threads, F32Smem<DH, RG>::kCtas)
+paged_f32_kernel(PagedAttnArgs a, int TB, Mark* marks, float* slots) {
+  using S = F32Smem<DH, RG>;
+  constexpr int RB = S::RB, kSteps = S::kPerWarp / 32, kVec = DH / 32;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   S& sm = *reinterpret_cast<S*>(smem_raw);
   const PagedBatch& p = a.p;
-  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+  const int tid = threadIdx.x, warp = tid >> 5, ty = (tid >> 3) & 3, tx = tid & 7;
+  const int r0 = warp % RG * 16 + ty, part = warp / RG, k0 = part * S::kPerWarp;  // first row, part, its first key
   const int G = a.Hq / p.Hkv;
   const Split sp{TB, kF32ItemCost, kF32Slack};
   pdl_wait();
@@ -60,153 +82,219 @@ __global__ void __launch_bounds__(kF32Threads) paged_f32_kernel(PagedAttnArgs a,
   if (!sm.st.any) return;
   const float sl2 = a.scale * 1.4426950408889634f;
   const float* Q = reinterpret_cast<const float*>(a.Q);
+  const float minf = -INFINITY;
 
   for (WalkT<false> w(sp, &sm.st); w.more(); w.next(p, sp)) {
     const Seq& s = w.s;
-    const int tb0 = w.i * TB;
+    const int tb0 = w.i * TB, tend = w.t0 + w.n;
+    const int rows = min(TB, s.nq - tb0) * G;  // that exist
+    const int last = s.len - s.nq + min(tb0 + TB, s.nq) - 1;  // the block's last visible position
+    auto locate = [&](int t) -> int64_t {  // this thread's entry of `row`
+      if (t < s.nm) {
+        const int sg = t * kTileSegs + tid / kSegRows, x = tid % kSegRows;
+        if (sg < p.Smax && x < __ldg(a.seg_cnt + w.b * p.Smax + sg))
+          return ((int64_t)(__ldg(a.seg_row + w.b * p.Smax + sg) + x) * p.Hkv + w.g) * DH;
+        return -1;
+      }
+      const int at = (t - s.nm) * kKeys + tid;
+      if (at > last) return -1;
+      const int pi = at / p.page;
+      const int64_t pg = __ldg(p.table + w.b * p.max_pages + pi);
+      if (pg >= 0 && pg < p.num_pages) return pg * a.page_stride + (at - pi * p.page) * a.row_stride + w.g * a.head_stride;
+      raise_flag(p.err_flag, MSA_FLAG_INDEX_OOB);
+      return -1;
+    };
+    // Tile t of K or V; keys that do not exist are zeros.
+    auto copy = [&](float (*dst)[DH + 4], const void* local, const void* bank, int t) {
+      const float* src = reinterpret_cast<const float*>(t < s.nm ? bank : local);
+      const int64_t* row = sm.row[(t - w.t0) & 1];
+#pragma unroll
+      for (int e = tid; e < kKeys * (DH / 4); e += kF32Threads) {
+        const int r = e / (DH / 4), c = e % (DH / 4) * 4;
+        const int64_t off = row[r];
+        cp_async16(&dst[r][c], off >= 0 ? src + off + c : Q, off >= 0);
+      }
+    };
     __syncthreads();  // the previous segment's readers are done
     for (int e = tid; e < RB * (DH / 4); e += kF32Threads) {
-      const int r = e / (DH / 4), c = (e - r * (DH / 4)) * 4;
-      const int t = tb0 + r / G;
+      const int r = e / (DH / 4), c = e % (DH / 4) * 4;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (r < TB * G && t < s.nq)
-        v = __ldg(reinterpret_cast<const float4*>(Q + (s.q0 + t) * a.q_ts + (w.g * G + r % G) * DH + c));
+      if (r < rows) v = __ldg(reinterpret_cast<const float4*>(Q + (s.q0 + tb0 + r / G) * a.q_ts + (w.g * G + r % G) * DH + c));
       *reinterpret_cast<float4*>(&sm.Q[r][c]) = v;
     }
-    int pos[RPT];  // last visible cache position of this thread's rows
-    float m_run[RPT], l_run[RPT], o[RPT][DPT];
+    if (tid < kKeys) sm.row[0][tid] = locate(w.t0);
+    __syncthreads();
+    copy(sm.K, a.K, a.Kbar, w.t0);
+    int pos[4];  // last visible cache position of this thread's rows
+    float m_run[4], l_run[4];
+    uint64_t o[4][2 * kVec];  // pairs
 #pragma unroll
-    for (int j = 0; j < RPT; ++j) {
-      const int r = ty * RPT + j, t = tb0 + r / G;
-      pos[j] = r < TB * G && t < s.nq ? s.len - s.nq + t : -1;
-      m_run[j] = -INFINITY;
-      l_run[j] = 0.f;
+    for (int j = 0; j < 4; ++j) {
+      const int r = r0 + 4 * j;
+      pos[j] = r < rows ? s.len - s.nq + tb0 + r / G : -1;
+      m_run[j] = minf;
+      l_run[j] = 0.f;  // over this thread's keys
 #pragma unroll
-      for (int c = 0; c < DPT; ++c) o[j][c] = 0.f;
+      for (int c = 0; c < 2 * kVec; ++c) o[j][c] = 0;
     }
-    const int last = s.len - s.nq + min(tb0 + TB, s.nq) - 1;  // the block's last visible position
 
-    for (int t = w.t0; t < w.t0 + w.n; ++t) {
+    for (int t = w.t0; t < tend; ++t) {
+      const int buf = (t - w.t0) & 1;
       const bool mem = t < s.nm;
-      const int key0 = mem ? 0 : (t - s.nm) * kKeys;
-      if (tid < kKeys) {
-        int64_t off = -1;
-        if (mem) {
-          const int sg = t * kTileSegs + tid / kSegRows, x = tid % kSegRows;
-          if (sg < p.Smax && x < __ldg(a.seg_cnt + w.b * p.Smax + sg))
-            off = ((int64_t)(__ldg(a.seg_row + w.b * p.Smax + sg) + x) * p.Hkv + w.g) * DH;
-        } else if (key0 + tid <= last) {
-          const int at = key0 + tid, pi = at / p.page;
-          const int64_t pg = __ldg(p.table + w.b * p.max_pages + pi);
-          if (pg >= 0 && pg < p.num_pages)
-            off = pg * a.page_stride + (at - pi * p.page) * a.row_stride + w.g * a.head_stride;
-          else
-            raise_flag(p.err_flag, MSA_FLAG_INDEX_OOB);
-        }
-        sm.row[tid] = off;
-      }
-      const float* Ksrc = reinterpret_cast<const float*>(mem ? a.Kbar : a.K);
-      const float* Vsrc = reinterpret_cast<const float*>(mem ? a.Vbar : a.V);
-      for (int k0 = 0; k0 < kKeys; k0 += kSub) {
-        if (!mem && key0 + k0 > last) break;
-        __syncthreads();  // rows written; the previous step's K, V and P are read
-        for (int e = tid; e < kSub * (DH / 4); e += kF32Threads) {
-          const int r = e / (DH / 4), c = (e - r * (DH / 4)) * 4;
-          const int64_t off = sm.row[k0 + r];
-          float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
-          if (off >= 0) {
-            kv = __ldg(reinterpret_cast<const float4*>(Ksrc + off + c));
-            vv = __ldg(reinterpret_cast<const float4*>(Vsrc + off + c));
+      const int key0 = (mem ? 0 : (t - s.nm) * kKeys) + k0;
+      const bool live = mem || key0 <= last;  // the warp's part has a visible key
+      cp_async_wait();
+      __syncthreads();  // K is here; V and the other half of `row` are read
+      copy(sm.V, a.V, a.Vbar, t);
+      if (t + 1 < tend && tid < kKeys) sm.row[buf ^ 1][tid] = locate(t + 1);
+      float (&P)[16][S::kPerWarp + 8] = sm.P[warp];
+      bool all = true;  // every row of the warp sees every key of its part
+      if (live) {
+        float sc[kSteps][4][4];
+#pragma unroll
+        for (int st = 0; st < kSteps; ++st) {
+          uint64_t acc[4][4];  // sums over the even and the odd dimensions
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[j][i] = 0;
+#pragma unroll 8
+          for (int c = 0; c < DH; c += 4) {
+            ulonglong2 k[4], q[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) k[i] = *reinterpret_cast<const ulonglong2*>(&sm.K[k0 + st * 32 + tx + 8 * i][c]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) q[j] = *reinterpret_cast<const ulonglong2*>(&sm.Q[r0 + 4 * j][c]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) acc[j][i] = f2_fma(q[j].y, k[i].y, f2_fma(q[j].x, k[i].x, acc[j][i]));
           }
-          *reinterpret_cast<float4*>(&sm.K[r][c]) = kv;
-          *reinterpret_cast<float4*>(&sm.V[r][c]) = vv;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float x, y;
+              f2_unpack(acc[j][i], x, y);
+              sc[st][j][i] = x + y;
+            }
         }
-        __syncthreads();
-        float sc[RPT][2];
+        float top[4];
 #pragma unroll
-        for (int j = 0; j < RPT; ++j) sc[j][0] = sc[j][1] = 0.f;
-#pragma unroll 4
-        for (int c = 0; c < DH; c += 4) {
-          const float4 ka = *reinterpret_cast<const float4*>(&sm.K[tx][c]);
-          const float4 kb = *reinterpret_cast<const float4*>(&sm.K[tx + 16][c]);
+        for (int j = 0; j < 4; ++j) top[j] = minf;
 #pragma unroll
-          for (int j = 0; j < RPT; ++j) {
-            const float4 q = *reinterpret_cast<const float4*>(&sm.Q[ty * RPT + j][c]);
-            sc[j][0] = fmaf(q.x, ka.x, fmaf(q.y, ka.y, fmaf(q.z, ka.z, fmaf(q.w, ka.w, sc[j][0]))));
-            sc[j][1] = fmaf(q.x, kb.x, fmaf(q.y, kb.y, fmaf(q.z, kb.z, fmaf(q.w, kb.w, sc[j][1]))));
+        for (int st = 0; st < kSteps; ++st)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int k = st * 32 + tx + 8 * i;
+            const bool have = sm.row[buf][k0 + k] >= 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const bool sees = have && (mem || key0 + k <= pos[j]);
+              all = all && sees;
+              if (!sees) sc[st][j][i] = minf;
+              top[j] = fmaxf(top[j], sc[st][j][i]);
+            }
           }
-        }
-        const bool ha = sm.row[k0 + tx] >= 0, hb = sm.row[k0 + tx + 16] >= 0;
-        const int pa = key0 + k0 + tx, pb = pa + 16;
+        all = __all_sync(0xffffffffu, all);
 #pragma unroll
-        for (int j = 0; j < RPT; ++j) {
-          if (!(ha && (mem || pa <= pos[j]))) sc[j][0] = -INFINITY;
-          if (!(hb && (mem || pb <= pos[j]))) sc[j][1] = -INFINITY;
-          float mx = fmaxf(sc[j][0], sc[j][1]);
+        for (int j = 0; j < 4; ++j) {
 #pragma unroll
-          for (int x = 8; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-          const float m_new = fmaxf(m_run[j], mx);
+          for (int x = 4; x > 0; x >>= 1) top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], x));
+          const float m_new = fmaxf(m_run[j], top[j]);
           // a row that has seen no key yet keeps weight 0 for everything
-          const float corr = m_run[j] == -INFINITY ? 0.f : exp2f((m_run[j] - m_new) * sl2);
-          const float e0 = sc[j][0] == -INFINITY ? 0.f : exp2f((sc[j][0] - m_new) * sl2);
-          const float e1 = sc[j][1] == -INFINITY ? 0.f : exp2f((sc[j][1] - m_new) * sl2);
-          float sum = e0 + e1;
-#pragma unroll
-          for (int x = 8; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-          l_run[j] = l_run[j] * corr + sum;
+          const float corr = m_run[j] == minf ? 0.f : exp2f((m_run[j] - m_new) * sl2);
           m_run[j] = m_new;
+          l_run[j] *= corr;
 #pragma unroll
-          for (int c = 0; c < DPT; ++c) o[j][c] *= corr;
-          sm.P[ty * RPT + j][tx] = e0;
-          sm.P[ty * RPT + j][tx + 16] = e1;
+          for (int st = 0; st < kSteps; ++st)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float e = sc[st][j][i] == minf ? 0.f : exp2f((sc[st][j][i] - m_new) * sl2);
+              l_run[j] += e;
+              P[ty + 4 * j][st * 32 + tx + 8 * i] = e;
+            }
+#pragma unroll
+          for (int c = 0; c < 2 * kVec; ++c) o[j][c] = f2_mul(o[j][c], f2_pack(corr, corr));
         }
-        __syncwarp();  // a row's weights are written and read by the same 16 lanes
-        for (int kc = 0; kc < kSub; kc += 4) {
-          float4 pr[RPT];
+      }
+      cp_async_wait();
+      __syncthreads();  // V and the next tile's places are here, K is read
+      if (t + 1 < tend) copy(sm.K, a.K, a.Kbar, t + 1);
+      auto add_values = [&](auto all) {  // all: every weight is of a key that its row sees
+#pragma unroll 2
+        for (int kc = 0; kc < S::kPerWarp; kc += 4) {
+          float4 pr[4];
 #pragma unroll
-          for (int j = 0; j < RPT; ++j) pr[j] = *reinterpret_cast<const float4*>(&sm.P[ty * RPT + j][kc]);
+          for (int j = 0; j < 4; ++j) pr[j] = *reinterpret_cast<const float4*>(&P[ty + 4 * j][kc]);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            // weight 0 keeps a masked key out even where its value is not finite
-            float v[DPT];
+            ulonglong2 v[kVec];
 #pragma unroll
-            for (int c = 0; c < DPT; c += 4) {
-              const float4 x = *reinterpret_cast<const float4*>(&sm.V[kc + q][(c / 4) * 64 + tx * 4]);
-              v[c] = x.x; v[c + 1] = x.y; v[c + 2] = x.z; v[c + 3] = x.w;
-            }
+            for (int c = 0; c < kVec; ++c) v[c] = *reinterpret_cast<const ulonglong2*>(&sm.V[k0 + kc + q][c * 32 + tx * 4]);
 #pragma unroll
-            for (int j = 0; j < RPT; ++j) {
+            for (int j = 0; j < 4; ++j) {
               const float pw = q == 0 ? pr[j].x : q == 1 ? pr[j].y : q == 2 ? pr[j].z : pr[j].w;
+              if (!all && pw == 0.f) continue;  // keeps a masked key out even where its value is not finite
+              const uint64_t p2 = f2_pack(pw, pw);
 #pragma unroll
-              for (int c = 0; c < DPT; ++c) o[j][c] = pw == 0.f ? o[j][c] : fmaf(pw, v[c], o[j][c]);
+              for (int c = 0; c < kVec; ++c) {
+                o[j][2 * c] = f2_fma(p2, v[c].x, o[j][2 * c]);
+                o[j][2 * c + 1] = f2_fma(p2, v[c].y, o[j][2 * c + 1]);
+              }
             }
           }
         }
+      };
+      if (live) {
+        if (all) add_values(std::true_type());
+        else add_values(std::false_type());
       }
-      __syncthreads();  // this tile's rows are read before the next tile's are written
     }
 
+    // the parts of a row, in their order; a sum of 0 is a part whose keys the row did not see
+    float (*parts)[DH] = reinterpret_cast<float (*)[DH]>(&sm.K[0][0]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+      for (int x = 4; x > 0; x >>= 1) l_run[j] += __shfl_xor_sync(0xffffffffu, l_run[j], x);
+      const int r = r0 + 4 * j;
+#pragma unroll
+      for (int c = 0; c < kVec; ++c)
+        *reinterpret_cast<ulonglong2*>(&parts[part * RB + r][c * 32 + tx * 4]) = make_ulonglong2(o[j][2 * c], o[j][2 * c + 1]);
+      if (tx == 0) sm.ml[part][r] = make_float2(m_run[j], l_run[j]);
+    }
+    __syncthreads();
     const bool whole = w.whole();
     float* slot = slots + slot_of(blockIdx.x, w.f, sm.st.f0) * slot_floats(RB, DH);
+    for (int e = tid; e < rows * (DH / 4); e += kF32Threads) {
+      const int r = e / (DH / 4), c = e % (DH / 4) * 4;
+      float top = minf, sum = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int j = 0; j < RPT; ++j) {
-      const int r = ty * RPT + j, t = tb0 + r / G;
-      if (r >= TB * G || t >= s.nq) continue;
-      const int h = w.g * G + r % G;
-      // the sum is 0 only where no key was visible: such a row is 0, its log-sum-exp -inf
-      const float inv = whole ? (l_run[j] == 0.f ? 0.f : 1.f / l_run[j]) : 1.f;
-      float* dst = whole ? reinterpret_cast<float*>(a.O) + ((s.q0 + t) * a.Hq + h) * DH : slot + r * DH;
+      for (int x = 0; x < S::kParts; ++x) top = fmaxf(top, sm.ml[x][r].x);
 #pragma unroll
-      for (int c = 0; c < DPT; c += 4)
-        *reinterpret_cast<float4*>(dst + (c / 4) * 64 + tx * 4) =
-            make_float4(o[j][c] * inv, o[j][c + 1] * inv, o[j][c + 2] * inv, o[j][c + 3] * inv);
-      if (tx == 0) {
-        if (!whole) {
-          slot[RB * DH + 2 * r] = m_run[j];
-          slot[RB * DH + 2 * r + 1] = l_run[j];
-        } else if (a.lse) {
-          a.lse[(int64_t)h * p.N + s.q0 + t] = l_run[j] == 0.f ? -INFINITY : m_run[j] * a.scale + logf(l_run[j]);
-        }
+      for (int x = 0; x < S::kParts; ++x) {
+        const float2 ml = sm.ml[x][r];
+        if (ml.y == 0.f) continue;
+        const float f = exp2f((ml.x - top) * sl2);
+        const float4 v = *reinterpret_cast<const float4*>(&parts[x * RB + r][c]);
+        sum += ml.y * f;
+        acc.x = fmaf(v.x, f, acc.x);
+        acc.y = fmaf(v.y, f, acc.y);
+        acc.z = fmaf(v.z, f, acc.z);
+        acc.w = fmaf(v.w, f, acc.w);
+      }
+      const int tk = tb0 + r / G, h = w.g * G + r % G;
+      if (whole) {
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.O) + ((s.q0 + tk) * a.Hq + h) * DH + c) =
+            make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        if (a.lse && c == 0)
+          a.lse[(int64_t)h * p.N + s.q0 + tk] = sum == 0.f ? minf : top * a.scale + logf(sum);
+      } else {
+        *reinterpret_cast<float4*>(slot + r * DH + c) = acc;
+        if (c == 0) *reinterpret_cast<float2*>(slot + RB * DH + 2 * r) = make_float2(top, sum);
       }
     }
   }
@@ -378,7 +466,7 @@ struct RowsSmem {
   float Q[16][DH];
   float part[8][RW][DH];
   float2 ml[8][RW];
-  int64_t row[2][kKeys];  // as in F32Smem, of this tile and the next
+  int64_t row[2][kKeys];  // as in F32Smem
   Start st;
 };
 
@@ -568,8 +656,14 @@ __global__ void __launch_bounds__(kF32Threads, 1) paged_f32_rows_kernel(PagedAtt
   }
 }
 
-// CTAs of the fp32 kernels per SM, by their registers and shared memory.
-int f32_ctas(bool few) { return few ? 1 : 2; }
+// Rows of a block of the fp32 block kernel.  64 where 32 hold less than half as many tokens, and for
+// heads of 128 where the blocks of 64 are at least twice the SMs (1,050 tokens x 32 heads over 2,200
+// keys 887 us, with 32 rows 981); else 32 (100 tokens over 1,100 keys 89 us, with 64 rows 100; heads
+// of 64, 1,050 tokens 525 us and 545).
+int f32_block_rows(int Hq, int Hkv, int d, int64_t N) {
+  const int G = Hq / Hkv;
+  return 64 / G > 2 * (32 / G) || (d == 128 && N * Hq >= 2 * 64 * (int64_t)sm_count()) ? 64 : 32;
+}
 
 template <typename Kernel, typename... Args>
 cudaError_t f32_launch(Kernel kernel, size_t smem, std::atomic<uint64_t>& done, int grid, int rows,
@@ -583,22 +677,26 @@ cudaError_t f32_launch(Kernel kernel, size_t smem, std::atomic<uint64_t>& done, 
   if (e != cudaSuccess) return e;
   return launch_merge(MSA_F32, false, MergeArgs{a, marks, slots, grid, rows, a.scale * 1.4426950408889634f}, s);
 }
-template <int DH>
+template <int DH, int RG>
 cudaError_t f32_block(const PagedAttnArgs& a, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
-  return f32_launch(paged_f32_kernel<DH>, sizeof(F32Smem<DH>), done, f32_ctas(false) * sm_count(), F32Smem<DH>::RB, a, s,
-                    F32Smem<DH>::RB / (a.Hq / a.p.Hkv));
+  return f32_launch(paged_f32_kernel<DH, RG>, sizeof(F32Smem<DH, RG>), done, F32Smem<DH, RG>::kCtas * sm_count(), 16 * RG,
+                    a, s, 16 * RG / (a.Hq / a.p.Hkv));
+}
+template <int DH>
+cudaError_t f32_blocks(const PagedAttnArgs& a, cudaStream_t s) {
+  return f32_block_rows(a.Hq, a.p.Hkv, DH, a.p.N) == 32 ? f32_block<DH, 2>(a, s) : f32_block<DH, 4>(a, s);
 }
 template <int DH, int RW, int kHalves>
-cudaError_t f32_rows(const PagedAttnArgs& a, cudaStream_t s) {
+cudaError_t f32_stream(const PagedAttnArgs& a, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
   return f32_launch(paged_f32_rows_kernel<DH, RW, kHalves>, sizeof(RowsSmem<DH, RW, kHalves>), done,
-                    f32_ctas(true) * sm_count(), 16, a, s);
+                    sm_count(), 16, a, s);
 }
 template <int DH>
 cudaError_t f32_few(const PagedAttnArgs& a, cudaStream_t s) {
   const int R = a.Hq / a.p.Hkv * a.p.max_q;
-  return R <= 4 ? f32_rows<DH, 4, 1>(a, s) : R <= 8 ? f32_rows<DH, 8, 1>(a, s) : f32_rows<DH, 8, 2>(a, s);
+  return R <= 4 ? f32_stream<DH, 4, 1>(a, s) : R <= 8 ? f32_stream<DH, 8, 1>(a, s) : f32_stream<DH, 8, 2>(a, s);
 }
 
 // Few rows per KV head: the kernels that hold at most 16 of them.
@@ -620,16 +718,17 @@ cudaError_t launch_merge(msa_dtype dt, bool quads, const MergeArgs& m, cudaStrea
 
 size_t paged_attn_partial_bytes(msa_dtype dt, int Hq, int Hkv, int d, int max_q) {
   const bool few = paged::few_rows(Hq, Hkv, max_q);
-  const int grid = dt == MSA_F32 ? paged::f32_ctas(few) * sm_count() : sm_count();
-  const int rows = dt == MSA_F32 ? (few ? 16 : 64) : (few ? Hq / Hkv * max_q : 128);
+  // fp32 blocks: as many rows with two CTAs of 32 per SM as with one of 64
+  const int grid = dt == MSA_F32 && !few ? 2 * sm_count() : sm_count();
+  const int rows = dt == MSA_F32 ? (few ? 16 : 32) : (few ? Hq / Hkv * max_q : 128);
   return paged::marks_bytes(grid) + 2 * (size_t)grid * paged::slot_floats(rows, d) * sizeof(float);
 }
 
 cudaError_t launch_paged_attn(msa_dtype dt, const PagedAttnArgs& a, cudaStream_t s) {
   const bool few = paged::few_rows(a.Hq, a.p.Hkv, a.p.max_q);
   if (dt == MSA_F32) {
-    if (a.d == 64) return few ? paged::f32_few<64>(a, s) : paged::f32_block<64>(a, s);
-    return few ? paged::f32_few<128>(a, s) : paged::f32_block<128>(a, s);
+    if (a.d == 64) return few ? paged::f32_few<64>(a, s) : paged::f32_blocks<64>(a, s);
+    return few ? paged::f32_few<128>(a, s) : paged::f32_blocks<128>(a, s);
   }
   return few ? launch_paged_decode(a, s) : launch_paged_prefill(a, s);
 }

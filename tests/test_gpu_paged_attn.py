@@ -99,6 +99,17 @@ def test_long_caches(dtype, q_len, total, Hq, Hkv, d):
     b.check(O, lse)
 
 
+@pytest.mark.parametrize("q_len,total,Hq,Hkv,d", [
+    ([300, 320], [420, 320], 32, 8, 128), ([20, 3], [180, 131], 20, 1, 64), ([9], [140], 33, 1, 128),
+    ([5, 70], [300, 70], 64, 1, 64), ([30, 40], [33, 500], 6, 2, 64), ([33], [129], 32, 1, 128)])
+def test_fp32_blocks_of_either_size(q_len, total, Hq, Hkv, d):
+    """Blocks of 32 rows and of 64, chosen by the heads that fit and the size of the batch."""
+    b = Batch(q_len, total, Hq, Hkv, d, 32, F32, DEV, seed=31).select(2, 9, 11, seed=8)
+    O, lse, flag = b.run(20)
+    assert _flag(flag) in (0, msa.FLAG_OVERFLOW)
+    b.check(O, lse, 20)
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_single_tokens_in_a_batch_with_parts(d):
     """Long runs of tiles where most rows of a block do not exist (their warps run ahead)."""
