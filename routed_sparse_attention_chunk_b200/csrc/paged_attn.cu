@@ -40,13 +40,14 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src, bool have
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // The block kernel.  RG groups of 16 query rows times 8 / RG parts of a tile's 128 keys, a warp
-// each: a thread keeps a 4 x 4 block of scores per 32 keys (rows ty + 4 j, keys tx + 8 i; 8 shared
-// memory wavefronts per 64 FMA instructions) and 4 x DH / 8 values of the output.  Every warp has
-// running maxima and sums of its own over its keys, merged at the segment's end, so its weights
-// never leave it.  K of the next tile is copied while P V runs, V while Q K^T does.  Bound by FMA
-// issue and shared memory together: two values an instruction (f32x2), and no question about a key
-// per FMA where the warp sees its whole part, took 1,050 tokens x 32 heads over 2,200 keys from 1,231
-// to 887 us, 43 TFLOP/s; blocks of 64 rows x 32 keys with 4 x 2 scores a thread had taken 1,127.
+// each: a thread keeps 4 rows (ty + 4 j) x 4 or 8 keys (tx + 8 i) of the scores and 4 x DH / 8
+// values of the output.  Every warp has running maxima and sums of its own over its keys, merged at
+// the segment's end, so its weights never leave it.  K of the next tile is copied while P V runs, V
+// while Q K^T does.  Bound by what shared memory can bring into registers (128 bytes a clock for
+// 128 FMA: 12 loads of 16 bytes per 128 FMA of a thread in Q K^T, 20 per 256 in P V): 1,050 tokens x
+// 32 heads of 128 over 2,200 keys take 849 us, 45 TFLOP/s.  Scores of 4 x 4 at a time took 887, one
+// value an instruction instead of pairs (f32x2) and a question about the key at every weight 1,231,
+// blocks of 64 rows x 32 keys with 4 x 2 scores a thread 1,127.
 template <int DH, int RG>
 struct F32Smem {
   static constexpr int RB = 16 * RG;              // query rows
@@ -151,33 +152,36 @@ paged_f32_kernel(PagedAttnArgs a, int TB, Mark* marks, float* slots) {
       bool all = true;  // every row of the warp sees every key of its part
       if (live) {
         float sc[kSteps][4][4];
+        {
+          uint64_t acc[kSteps][4][4];  // sums over the even and the odd dimensions
 #pragma unroll
-        for (int st = 0; st < kSteps; ++st) {
-          uint64_t acc[4][4];  // sums over the even and the odd dimensions
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[j][i] = 0;
-#pragma unroll 8
+          for (int x = 0; x < kSteps * 16; ++x) acc[x / 16][x / 4 % 4][x % 4] = 0;
+#pragma unroll 16
           for (int c = 0; c < DH; c += 4) {
-            ulonglong2 k[4], q[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) k[i] = *reinterpret_cast<const ulonglong2*>(&sm.K[k0 + st * 32 + tx + 8 * i][c]);
+            ulonglong2 q[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) q[j] = *reinterpret_cast<const ulonglong2*>(&sm.Q[r0 + 4 * j][c]);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int st = 0; st < kSteps; ++st) {
+              ulonglong2 k[4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) acc[j][i] = f2_fma(q[j].y, k[i].y, f2_fma(q[j].x, k[i].x, acc[j][i]));
+              for (int i = 0; i < 4; ++i) k[i] = *reinterpret_cast<const ulonglong2*>(&sm.K[k0 + st * 32 + tx + 8 * i][c]);
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[st][j][i] = f2_fma(q[j].y, k[i].y, f2_fma(q[j].x, k[i].x, acc[st][j][i]));
+            }
           }
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+          for (int st = 0; st < kSteps; ++st)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float x, y;
-              f2_unpack(acc[j][i], x, y);
-              sc[st][j][i] = x + y;
-            }
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                float x, y;
+                f2_unpack(acc[st][j][i], x, y);
+                sc[st][j][i] = x + y;
+              }
         }
         float top[4];
 #pragma unroll
@@ -222,7 +226,7 @@ paged_f32_kernel(PagedAttnArgs a, int TB, Mark* marks, float* slots) {
       __syncthreads();  // V and the next tile's places are here, K is read
       if (t + 1 < tend) copy(sm.K, a.K, a.Kbar, t + 1);
       auto add_values = [&](auto all) {  // all: every weight is of a key that its row sees
-#pragma unroll 2
+#pragma unroll 4
         for (int kc = 0; kc < S::kPerWarp; kc += 4) {
           float4 pr[4];
 #pragma unroll
@@ -656,13 +660,13 @@ __global__ void __launch_bounds__(kF32Threads, 1) paged_f32_rows_kernel(PagedAtt
   }
 }
 
-// Rows of a block of the fp32 block kernel.  64 where 32 hold less than half as many tokens, and for
-// heads of 128 where the blocks of 64 are at least twice the SMs (1,050 tokens x 32 heads over 2,200
-// keys 887 us, with 32 rows 981); else 32 (100 tokens over 1,100 keys 89 us, with 64 rows 100; heads
-// of 64, 1,050 tokens 525 us and 545).
-int f32_block_rows(int Hq, int Hkv, int d, int64_t N) {
+// Rows of a block of the fp32 block kernel.  64 where 32 hold less than half as many tokens, and
+// where the blocks of 64 are at least twice the SMs (1,050 tokens x 32 heads over 2,200 keys: heads
+// of 128 849 us, with 32 rows 947; heads of 64 475 and 493); else 32, two CTAs per SM with heads of
+// 64 (100 tokens over 1,100 keys 86 us, with 64 rows 96).
+int f32_block_rows(int Hq, int Hkv, int64_t N) {
   const int G = Hq / Hkv;
-  return 64 / G > 2 * (32 / G) || (d == 128 && N * Hq >= 2 * 64 * (int64_t)sm_count()) ? 64 : 32;
+  return 64 / G > 2 * (32 / G) || N * Hq >= 2 * 64 * (int64_t)sm_count() ? 64 : 32;
 }
 
 template <typename Kernel, typename... Args>
@@ -685,7 +689,7 @@ cudaError_t f32_block(const PagedAttnArgs& a, cudaStream_t s) {
 }
 template <int DH>
 cudaError_t f32_blocks(const PagedAttnArgs& a, cudaStream_t s) {
-  return f32_block_rows(a.Hq, a.p.Hkv, DH, a.p.N) == 32 ? f32_block<DH, 2>(a, s) : f32_block<DH, 4>(a, s);
+  return f32_block_rows(a.Hq, a.p.Hkv, a.p.N) == 32 ? f32_block<DH, 2>(a, s) : f32_block<DH, 4>(a, s);
 }
 template <int DH, int RW, int kHalves>
 cudaError_t f32_stream(const PagedAttnArgs& a, cudaStream_t s) {
