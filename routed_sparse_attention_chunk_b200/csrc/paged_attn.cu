@@ -43,11 +43,12 @@ __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_al
 // each: a thread keeps 4 rows (ty + 4 j) x 4 or 8 keys (tx + 8 i) of the scores and 4 x DH / 8
 // values of the output.  Every warp has running maxima and sums of its own over its keys, merged at
 // the segment's end, so its weights never leave it.  K of the next tile is copied while P V runs, V
-// while Q K^T does.  Bound by what shared memory can bring into registers (128 bytes a clock for
-// 128 FMA: 12 loads of 16 bytes per 128 FMA of a thread in Q K^T, 20 per 256 in P V): 1,050 tokens x
-// 32 heads of 128 over 2,200 keys take 849 us, 45 TFLOP/s.  Scores of 4 x 4 at a time took 887, one
-// value an instruction instead of pairs (f32x2) and a question about the key at every weight 1,231,
-// blocks of 64 rows x 32 keys with 4 x 2 scores a thread 1,127.
+// while Q K^T does.  1,050 tokens x 32 heads of 128 over 2,200 keys take 849 us, 45 TFLOP/s: shared
+// memory's way into the registers (128 bytes a clock for 128 FMA; 12 loads of 16 bytes per 128 FMA of
+// a thread in Q K^T, 20 per 256 in P V) is 61 % busy, the FMA pipe 50 %, the rest latencies of two
+// warps per scheduler.  Scores of 4 x 4 at a time took 887 us, one value an instruction instead of
+// pairs (f32x2) and a question about the key at every weight 1,231, blocks of 64 rows x 32 keys with
+// 4 x 2 scores a thread 1,127.
 template <int DH, int RG>
 struct F32Smem {
   static constexpr int RB = 16 * RG;              // query rows
