@@ -342,6 +342,22 @@ def test_values_that_are_not_finite(dtype, q_len, total, d, max_q):
     assert O2[:b2.N][hit].isnan().all() and torch.equal(O2[:b2.N][~hit], O1[:b2.N][~hit])
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("q_len,total,d", [([3, 1], [300, 140], 128), ([1, 2], [700, 40], 64), ([150, 4], [200, 600], 128),
+                                           ([70], [300], 64)])
+def test_query_that_is_not_finite(dtype, q_len, total, d):
+    """A head of a token whose query holds a NaN is NaN; no other head or token changes by a bit."""
+    b = Batch(q_len, total, 8, 2, d, 16, dtype, DEV, seed=41)
+    O1, lse1, _ = b.run()
+    tok, h = b.N // 2, 5
+    b.Q[tok, h, 7] = float("nan")
+    O2, lse2, flag = b.run()
+    assert _flag(flag) == 0
+    assert O2[tok, h].isnan().all() and lse2[h, tok].isnan()
+    O2[tok, h], lse2[h, tok] = O1[tok, h], lse1[h, tok]
+    assert torch.equal(O1, O2) and torch.equal(lse1, lse2)
+
+
 @pytest.mark.parametrize("dtype,max_q", [(F32, 1), (BF, 1), (BF, 40)])
 def test_no_new_tokens_at_all(dtype, max_q):
     """Sequences without new tokens leave everything as it was; rows before the first are nobody's."""
