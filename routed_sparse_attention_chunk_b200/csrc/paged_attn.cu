@@ -312,102 +312,93 @@ paged_f32_kernel(PagedAttnArgs a, int TB, Mark* marks, float* slots) {
 constexpr int kMergeThreads = 256, kMergeRows = 32;
 constexpr int kAtOnce = 8;  // segments whose loads are in flight together
 
-// The whole batch on the CUDA cores, for bf16 batches with values that are not finite among keys
-// that only some rows see.  Half a warp takes one (token, head) row at a time, a lane DH / 16 of
-// its dimensions, and goes through the keys the row sees with a running maximum and sum.  A key
-// that it does not see is never read; one that it sees keeps a weight above 0, so that an infinity
-// stays one.  Slow, and without shared memory: the merging blocks sit beside the kernel they wait for.
-template <int DH>
-__device__ __forceinline__ void attend_all(const PagedAttnArgs& a) {
-  constexpr int DPT = DH / 16;  // 4 or 8 bf16 values: 8 or 16 bytes
-  const PagedBatch& p = a.p;
-  const int G = a.Hq / p.Hkv, x0 = (threadIdx.x & 15) * DPT;
-  const float sl2 = a.scale * 1.4426950408889634f;
-  const int64_t me = ((int64_t)blockIdx.x + (int64_t)blockIdx.y * gridDim.x) * (kMergeThreads / 16) + (threadIdx.x >> 4);
-  const int64_t all = (int64_t)gridDim.x * gridDim.y * (kMergeThreads / 16);
-  auto load = [&](const void* base, int64_t off, float (&f)[DPT]) {
-    const __nv_bfloat162* src = reinterpret_cast<const __nv_bfloat162*>(reinterpret_cast<const __nv_bfloat16*>(base) + off + x0);
+// Row of the V pages of cache position `at` of sequence b for KV head g; null: its page is outside the pool.
+__device__ __forceinline__ const __nv_bfloat16* value_row(const PagedAttnArgs& a, int64_t b, int g, int at) {
+  const int pi = at / a.p.page;
+  const int64_t pg = __ldg(a.p.table + b * a.p.max_pages + pi);
+  if (pg < 0 || pg >= a.p.num_pages) return nullptr;
+  return reinterpret_cast<const __nv_bfloat16*>(a.V) + pg * a.page_stride + (at - pi * a.p.page) * a.row_stride + g * a.head_stride;
+}
+// The values that are not finite which an item's tiles left out (paged_tma.cuh): of the keys after its
+// first token's, to the rows that see them.
+// Four dimensions of the output of packed row `row`, for an item that is being merged:
+__device__ __forceinline__ void add_odd_to_row(const PagedAttnArgs& a, const Mark& mk, int64_t row, int quad,
+                                               float (&acc)[4]) {
+  const Seq s = load_seq(a.p, mk.b);
+  const int pos0 = s.len - s.nq, first = pos0 + (int)(mk.row - s.q0), pos = pos0 + (int)(row - s.q0);
+#pragma unroll 1
+  for (int key = max(first + 1, 0); key <= pos; ++key) {
+    const __nv_bfloat16* v = value_row(a, mk.b, mk.g, key);
+    if (!v) continue;
 #pragma unroll
-    for (int i = 0; i < DPT / 2; ++i) {
-      const float2 v = __bfloat1622float2(src[i]);
-      f[2 * i] = v.x;
-      f[2 * i + 1] = v.y;
+    for (int i = 0; i < 4; ++i) {
+      const float f = __bfloat162float(v[quad * 4 + i]);
+      if (!isfinite(f)) acc[i] += f;
     }
-  };
+  }
+}
+// ... and the outputs of all items that no mark names, which their CTA has written: a warp takes every
+// `warps`-th item, a lane its dimensions of a key's values.  Here, because the attention kernels run
+// slower the more code lies around their loops (23 requests with heads of 64: 120.6 us, with this at
+// each item's end 132, at the CTA's end 126), and not inlined, because the merge's registers spill
+// then (one token 11.5 us instead of 10.5).
+template <int DH>
+__device__ __noinline__ void add_odd_values(const MergeArgs& ma, int64_t warp, int64_t warps) {
+  constexpr int kEach = DH / 32;
+  const PagedAttnArgs& a = ma.a;
+  const PagedBatch& p = a.p;
+  const int lane = threadIdx.x & 31, G = a.Hq / p.Hkv;
+  int64_t turn = warp;  // items until this warp's next one
+#pragma unroll 1
   for (int64_t b = 0; b < p.B; ++b) {
     const Seq s = load_seq(p, b);
-    const int64_t rows = (int64_t)s.nq * a.Hq;
-    // the two halves of a warp step together: rows past the last are computed again, not written
-    for (int64_t x = me; (x & ~int64_t(1)) < rows; x += all) {
-      const int64_t r = min(x, rows - 1);
-      const int t = (int)(r / a.Hq), h = (int)(r - (int64_t)t * a.Hq), g = h / G;
-      const int local = max(0, s.len - s.nq + t + 1), mem = s.nm * kKeys;
-      float q[DPT], o[DPT], m = -INFINITY, l = 0.f;
-      load(a.Q, (s.q0 + t) * a.q_ts + h * DH, q);
-#pragma unroll
-      for (int i = 0; i < DPT; ++i) o[i] = 0.f;
-      const int keys = mem + local, most = max(keys, __shfl_xor_sync(0xffffffffu, keys, 16));
-      for (int k = 0; k < most; ++k) {
-        bool sees = k < keys;
-        const void *kb = a.K, *vb = a.V;
-        int64_t off = -1;
-        if (k < mem) {
-          const int sg = k / kSegRows;
-          sees = sg < p.Smax && k % kSegRows < __ldg(a.seg_cnt + b * p.Smax + sg);
-          if (sees) off = ((int64_t)(__ldg(a.seg_row + b * p.Smax + sg) + k % kSegRows) * p.Hkv + g) * DH;
-          kb = a.Kbar;
-          vb = a.Vbar;
-        } else if (sees) {
-          const int at = k - mem, pi = at / p.page;
-          const int64_t pg = __ldg(p.table + b * p.max_pages + pi);
-          if (pg >= 0 && pg < p.num_pages) off = pg * a.page_stride + (at - pi * p.page) * a.row_stride + g * a.head_stride;
-        }
-        float kf[DPT] = {}, vf[DPT] = {}, dot = 0.f;
-        if (off >= 0) {
-          load(kb, off, kf);
-          load(vb, off, vf);
-        }
-#pragma unroll
-        for (int i = 0; i < DPT; ++i) dot = fmaf(q[i], kf[i], dot);
-#pragma unroll
-        for (int y = 8; y > 0; y >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, y);
-        if (!sees) continue;
-        const float m_new = fmaxf(m, dot);
-        const float corr = m == -INFINITY ? 0.f : exp2f((m - m_new) * sl2), e = exp2f((dot - m_new) * sl2);
-        const float w = e < 1.17549435e-38f ? 1.17549435e-38f : e;  // (a NaN stays)
-        l = l * corr + w;
-        m = m_new;
-#pragma unroll
-        for (int i = 0; i < DPT; ++i) o[i] = fmaf(w, vf[i], corr == 0.f ? 0.f : o[i] * corr);
+    const int64_t items = (int64_t)blocks_of(s, ma.TB) * p.Hkv;
+    for (; turn < items; turn += warps) {
+      const int i = (int)(turn / p.Hkv), g = (int)(turn - (int64_t)i * p.Hkv), t0 = i * ma.TB;
+      bool merged = false;
+      for (int c = 1 + lane; c < ma.grid; c += 32) {
+        const Mark mk = ma.marks[c];
+        merged = merged || (mk.tokens > 0 && mk.b == b && mk.g == g && mk.row == s.q0 + t0);
       }
-      if (x >= rows) continue;
-      const int64_t out = s.q0 + t;
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(a.O) + (out * a.Hq + h) * DH + x0;
-#pragma unroll
-      for (int i = 0; i < DPT; ++i) dst[i] = __float2bfloat16_rn(l == 0.f ? 0.f : o[i] * inv);
-      if (a.lse && x0 == 0) a.lse[(int64_t)h * p.N + out] = l == 0.f ? -INFINITY : m * a.scale + logf(l);
+      if (__any_sync(0xffffffffu, merged)) continue;
+      const int rows = min(ma.TB, s.nq - t0) * G, first = s.len - s.nq + t0;
+      __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.O) + ((s.q0 + t0) * a.Hq + g * G) * DH;
+#pragma unroll 1
+      for (int key = max(first + 1, 0); key < s.len && (key - first) * G < rows; ++key) {
+        const __nv_bfloat16* v = value_row(a, b, g, key);
+        if (!v) continue;
+#pragma unroll 1
+        for (int x = 0; x < kEach; ++x) {
+          const float f = __bfloat162float(v[lane * kEach + x]);
+          for (unsigned odd = __ballot_sync(0xffffffffu, !isfinite(f)); odd; odd &= odd - 1) {
+            const int from = __ffs(odd) - 1;
+            const float add = __shfl_sync(0xffffffffu, f, from);
+            for (int r = lane; r < rows; r += 32) {  // a row stays with one lane, so its sums have one order
+              if (r < (key - first) * G) continue;
+              __nv_bfloat16* dst = out + ((int64_t)(r / G) * a.Hq + r % G) * DH + from * kEach + x;
+              *dst = __float2bfloat16_rn(__bfloat162float(*dst) + add);
+            }
+          }
+        }
+      }
     }
+    turn -= items;
   }
 }
 
 template <typename T, int DH, bool kQuads>
-__global__ void __launch_bounds__(kMergeThreads, 4) merge_kernel(MergeArgs ma) {
+__global__ void __launch_bounds__(kMergeThreads, 4) merge_kernel(const __grid_constant__ MergeArgs ma) {
   constexpr int kPairs = kMergeRows * (DH / 4);  // (row, four values) pairs of the block
   pdl_wait();
   const PagedAttnArgs& a = ma.a;
   const Mark mk = ma.marks[blockIdx.x + 1];
-  if constexpr (sizeof(T) == 2) {
-    if (any_odd(ma.marks, ma.grid)) {  // the same in every warp
-      attend_all<DH>(a);
-      return;
-    }
-  }
+  bool odd = false;  // values may have been left out
+  if constexpr (sizeof(T) == 2) odd = any_odd(ma.marks, ma.grid);
   const int G = a.Hq / a.p.Hkv;
   const int last = mk.tokens * G;  // rows of the item
   const size_t sf = slot_floats(ma.rows, DH);
-  const float* first = ma.slots + (2 * mk.c0 + mk.late) * sf;
-  const float* rest = ma.slots + 2 * mk.c0 * sf;  // segment x > 0 is in slot 2 (c0 + x)
+  const float* first = ma.slots + (2 * (int64_t)mk.c0 + mk.late) * sf;
+  const float* rest = ma.slots + 2 * (int64_t)mk.c0 * sf;  // segment x > 0 is in slot 2 (c0 + x)
   for (int e = threadIdx.x; e < kPairs; e += kMergeThreads) {
     // consecutive threads: rows first in the quads layout, values of a row first in the other
     const int quad = kQuads ? e / kMergeRows : e % (DH / 4);
@@ -450,14 +441,20 @@ __global__ void __launch_bounds__(kMergeThreads, 4) merge_kernel(MergeArgs ma) {
     const int tl = r / G, h = mk.g * G + (r - tl * G);
     const int64_t row = mk.row + tl;
     T* dst = reinterpret_cast<T*>(a.O) + (row * a.Hq + h) * DH + quad * 4;
-    if constexpr (sizeof(T) == 4)
-      *reinterpret_cast<float4*>(dst) = make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
-    else
-      *reinterpret_cast<uint2*>(dst) =
-          make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] *= inv;
+    if constexpr (sizeof(T) == 4) {
+      *reinterpret_cast<float4*>(dst) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    } else {
+      if (odd) add_odd_to_row(a, mk, row, quad, acc);
+      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]));
+    }
     if (a.lse && quad == 0)
       a.lse[(int64_t)h * a.p.N + row] = seen ? (m * ma.unit_log2 + log2f(l)) * 0.69314718055994531f : -INFINITY;
   }
+  if (odd)
+    add_odd_values<DH>(ma, ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * (kMergeThreads / 32) + (threadIdx.x >> 5),
+                       (int64_t)gridDim.x * gridDim.y * (kMergeThreads / 32));
 }
 
 // fp32 for up to 16 rows per KV head, bound by HBM: 256 threads stream the tiles' rows straight
@@ -680,7 +677,7 @@ cudaError_t f32_launch(Kernel kernel, size_t smem, std::atomic<uint64_t>& done, 
   count_launch();
   e = launch_pdl(kernel, dim3((unsigned)grid), dim3(kF32Threads), smem, s, a, args..., marks, slots);
   if (e != cudaSuccess) return e;
-  return launch_merge(MSA_F32, false, MergeArgs{a, marks, slots, grid, rows, a.scale * 1.4426950408889634f}, s);
+  return launch_merge(MSA_F32, false, MergeArgs{a, marks, slots, grid, rows, 0, a.scale * 1.4426950408889634f}, s);
 }
 template <int DH, int RG>
 cudaError_t f32_block(const PagedAttnArgs& a, cudaStream_t s) {

@@ -128,7 +128,7 @@ paged_decode_kernel(const __grid_constant__ TileMaps maps, DecParams a) {
   uint64_t* drain = o_done + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_s = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  volatile int* odd_s = abort_s + 1;  // a value that is not finite (row_not_finite)
+  volatile int* odd_s = abort_s + 1;  // values were left out of a product (drop_not_finite)
   Start* start = reinterpret_cast<Start*>(bars + L::kBars);
 
   const PagedBatch& p = a.p;
@@ -366,7 +366,10 @@ paged_decode_kernel(const __grid_constant__ TileMaps maps, DecParams a) {
           hold(&kv_full[g % kStages], (g / kStages) & 1);
           uint8_t* vt = ring + (g % kStages) * L::kStage + L::kTile;
           if (mem ? low > 0 : key >= w.s.len) zero_row<DH>(vt, r_lane);
-          else if (!mem && key > pos0 && row_not_finite<DH>(vt, r_lane)) *odd_s = 1;
+          else if (!mem && key > pos0 && row_not_finite<DH>(vt, r_lane)) {
+            drop_not_finite<DH>(vt, r_lane);
+            *odd_s = 1;
+          }
           __syncwarp();
         }
         // The maximum moves only where a score passes it by 2^8 (always in the first tile with a
@@ -522,7 +525,7 @@ cudaError_t decode_t(const PagedAttnArgs& a, cudaStream_t s) {
   count_launch();
   e = launch_pdl(kern, dim3((unsigned)grid), dim3(kThreads), (size_t)L::kSmem, s, maps, d);
   if (e != cudaSuccess) return e;
-  return launch_merge(MSA_BF16, false, MergeArgs{a, d.marks, d.slots, grid, d.R, 1.f}, s);
+  return launch_merge(MSA_BF16, false, MergeArgs{a, d.marks, d.slots, grid, d.R, a.p.max_q, 1.f}, s);
 }
 
 }  // namespace

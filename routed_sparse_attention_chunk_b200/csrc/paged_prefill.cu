@@ -129,7 +129,7 @@ paged_prefill_kernel(const __grid_constant__ TileMaps maps, PreParams a) {
   static_assert(4 * kKV + 4 + 3 + 8 <= L::kBars - 2, "barriers");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + L::kBars - 2);
   volatile int* abort_s = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  volatile int* odd_s = abort_s + 1;  // a value that is not finite (row_not_finite)
+  volatile int* odd_s = abort_s + 1;  // values were left out of a product (drop_not_finite)
   float* m_s = reinterpret_cast<float*>(bars + L::kBars);     // [kRows] O's references, log2 domain
   float2* ml_s = reinterpret_cast<float2*>(m_s + kRows);      // [kRows] (reference, sum)
   Start* start = reinterpret_cast<Start*>(ml_s + kRows);
@@ -404,7 +404,10 @@ paged_prefill_kernel(const __grid_constant__ TileMaps maps, PreParams a) {
             uint8_t* vt = Vs + vs * L::kK;
             const int key = base + r;
             if (key >= w.s.len) zero_row<DH>(vt, r);
-            else if (key > first && row_not_finite<DH>(vt, r)) *odd_s = 1;
+            else if (key > first && row_not_finite<DH>(vt, r)) {
+              *odd_s = 1;
+              drop_not_finite<DH>(vt, r);
+            }
             fence_async_smem();
             __syncwarp();
           }
@@ -603,7 +606,7 @@ cudaError_t prefill_t(const PagedAttnArgs& a, cudaStream_t s) {
   count_launch();
   e = launch_pdl(paged_prefill_kernel<DH>, dim3((unsigned)grid), dim3(kThreads), (size_t)L::kSmem, s, maps, d);
   if (e != cudaSuccess) return e;
-  return launch_merge(MSA_BF16, true, MergeArgs{a, d.marks, d.slots, grid, kRows, 1.f}, s);
+  return launch_merge(MSA_BF16, true, MergeArgs{a, d.marks, d.slots, grid, kRows, d.TB, 1.f}, s);
 }
 
 }  // namespace

@@ -281,7 +281,8 @@ struct WalkT {
 // start of its share is the first to cut (tokens = 0: none).
 struct Mark {
   int64_t row;     // packed row of the item's first token
-  int64_t c0;      // CTA of its first segment
+  int32_t b;       // sequence
+  int32_t c0;      // CTA of its first segment
   int32_t n;       // segments, in CTAs c0 .. c0 + n - 1
   int32_t late;    // the first segment is its CTA's last one, not its first
   int32_t tokens;  // of the item
@@ -293,7 +294,8 @@ __device__ __forceinline__ void leave_mark(const Start* st, const Split& sp, int
   if (st->any && t > 0 && t <= st->per) {  // not cut at an earlier border already
     const int64_t end = st->f0 - t + block_tiles(st->s, sp.TB, st->i);
     v.row = st->s.q0 + (int64_t)st->i * sp.TB;
-    v.c0 = c - 1;
+    v.b = (int32_t)st->b;
+    v.c0 = (int32_t)(c - 1);
     v.late = st->o < st->per;
     v.n = 2;
     for (int64_t at = st->f1; at < end; at += st->per) ++v.n;
@@ -303,8 +305,8 @@ __device__ __forceinline__ void leave_mark(const Start* st, const Split& sp, int
   *m = v;
 }
 
-// Workspace: one Mark per CTA, one byte per CTA (whether it met values that are not finite among
-// keys that only some rows see), then two partial results per CTA.  A partial result of `rows`
+// Workspace: one Mark per CTA, one byte per CTA (whether it left out values that are not finite, of
+// keys that only some rows see: paged_tma.cuh), then two partial results per CTA.  A partial result of `rows`
 // rows is rows x DH unnormalised output values and rows x (row maximum, row sum), as floats.
 __host__ __device__ inline size_t marks_bytes(int grid) {
   return ((size_t)grid * (sizeof(Mark) + 1) + 16 + 255) / 256 * 256;
@@ -332,13 +334,14 @@ __host__ __device__ inline size_t slot_floats(int rows, int dh) {
 // segments can belong to cut items).
 __device__ __forceinline__ int64_t slot_of(int64_t c, int64_t f, int64_t f0) { return 2 * c + (f == f0 ? 0 : 1); }
 
-// The merging kernel (paged_attn.cu): O and lse of the items the marks name, or of the whole batch
-// if a CTA says odd.
+// The merging kernel (paged_attn.cu): O and lse of the items the marks name; and of all items, the
+// values that were left out of the products if a CTA says so.
 struct MergeArgs {
   PagedAttnArgs a;
   Mark* marks;
   const float* slots;
   int grid, rows;   // CTAs that left marks, rows of a slot
+  int TB;           // tokens of a block
   float unit_log2;  // row maxima times this are in the log2 domain
 };
 // quads: values (row, x) of a slot at (x / 4) * rows * 4 + row * 4 + x % 4 (a row per thread
