@@ -578,6 +578,7 @@ __global__ void __launch_bounds__(kF32Threads, 1) paged_f32_rows_kernel(PagedAtt
             top = fmaxf(top, sc[n]);
           }
           const float corr = m[r] == minf ? 0.f : exp2f((m[r] - top) * sl2);
+          const float ref = top == minf ? 0.f : top;  // nothing above -inf yet: keys of score -inf weigh 0
           m[r] = top;
           l[r] *= corr;
 #pragma unroll
@@ -585,7 +586,7 @@ __global__ void __launch_bounds__(kF32Threads, 1) paged_f32_rows_kernel(PagedAtt
 #pragma unroll
           for (int n = 0; n < kAhead; ++n) {
             if (!all && sc[n] == minf) continue;  // not seen: whatever V holds stays out
-            const float pw = exp2f((sc[n] - top) * sl2);
+            const float pw = exp2f((sc[n] - ref) * sl2);
             l[r] += pw;
 #pragma unroll
             for (int i = 0; i < kVec; ++i) {

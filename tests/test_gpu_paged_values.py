@@ -94,6 +94,12 @@ def test_keys_of_score_minus_infinity_weigh_nothing(q_len, total, d, max_q, keys
     _minus_infinity(BF, q_len, total, d, max_q, keys, poison)
 
 
+@pytest.mark.parametrize("poison", [False, True])
+@pytest.mark.parametrize("q_len,total,d,max_q,keys", MINUS_INF)
+def test_fp32_keys_of_score_minus_infinity_weigh_nothing(q_len, total, d, max_q, keys, poison):
+    _minus_infinity(F32, q_len, total, d, max_q, keys, poison)
+
+
 HARDLY = [([1], [300], 128), ([1], [300], 64), ([2], [300], 128), ([4], [300], 128), ([3], [40000], 128),
           ([70], [300], 128), ([70], [300], 64), ([130], [9000], 128)]
 
