@@ -635,7 +635,10 @@ msa_status msa_paged_append(msa_dtype dt, const void* q, int64_t q_tok_stride, v
  * A token that sees no key (a position before 0, no memory rows) gets O = 0 and
  * lse = -inf.  A key that a token does not see never reaches its output, whatever
  * its K and V rows hold (NaN and infinities included): later tokens, the rest of
- * a sequence's last page, the bank rows beside a selected run.
+ * a sequence's last page, the bank rows beside a selected run.  A value that is
+ * not finite makes the outputs that see it not finite in its dimension, however
+ * small its weight; a key of score -inf weighs nothing, and a row that sees no
+ * other key gets O = 0 and lse = -inf.
  * Supported: Hq % Hkv == 0, at most 64 query heads per KV head.  bf16 runs on the
  * tensor cores, fp32 in fp32.  The result does not depend on timing: partial sums
  * are merged in a fixed order.

@@ -215,7 +215,10 @@ paged_f32_kernel(PagedAttnArgs a, int TB, Mark* marks, float* slots) {
           for (int st = 0; st < kSteps; ++st)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const float e = sc[st][j][i] == minf ? 0.f : exp2f((sc[st][j][i] - m_new) * sl2);
+              // a weight of 0 below is a key that the row does not see, so one it sees keeps at least 2^-149
+              // (NaN is larger as an unsigned number and stays)
+              const float e = sc[st][j][i] == minf ? 0.f
+                            : __uint_as_float(max(__float_as_uint(exp2f((sc[st][j][i] - m_new) * sl2)), 1u));
               l_run[j] += e;
               P[ty + 4 * j][st * 32 + tx + 8 * i] = e;
             }
@@ -612,7 +615,7 @@ __global__ void __launch_bounds__(kF32Threads, 1) paged_f32_rows_kernel(PagedAtt
 #pragma unroll
         for (int c = 0; c < 4 * kVec; ++c) {
           const float y = __shfl_xor_sync(0xffffffffu, o[r][c], x);
-          o[r][c] = (f == 0.f ? 0.f : o[r][c] * f) + (fo == 0.f ? 0.f : y * fo);
+          o[r][c] = o[r][c] * f + y * fo;  // (0 where no key was seen; an infinity is not lost to a factor of 0)
         }
       }
       if (grp == 0) {

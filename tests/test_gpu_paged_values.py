@@ -133,3 +133,11 @@ def _hardly_weighs(dtype, q_len, total, d, where, val):
 @pytest.mark.parametrize("val", [INF, NAN])
 def test_a_value_that_hardly_weighs_is_still_seen(q_len, total, d, where, val):
     _hardly_weighs(BF, q_len, total, d, where, val)
+
+
+
+@pytest.mark.parametrize("q_len,total,d", HARDLY)
+@pytest.mark.parametrize("where", ["first", "middle", "new", "new_low_first"])
+@pytest.mark.parametrize("val", [INF, NAN])
+def test_fp32_a_value_that_hardly_weighs_is_still_seen(q_len, total, d, where, val):
+    _hardly_weighs(F32, q_len, total, d, where, val)
