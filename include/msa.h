@@ -595,6 +595,8 @@ msa_status msa_rope_backward(msa_dtype dt, const void* dout, int64_t dout_tok_st
  * Device flags of both: MSA_FLAG_OFFSETS for offsets that decrease or leave
  * [0, N], MSA_FLAG_INDEX_OOB for a page outside [0, num_pages) or a length
  * outside [0, max_pages * page].
+ * The attention reads such a page as zeros, such a length as the nearest one
+ * inside, and skips a sequence with such offsets.
  *
  * msa_paged_append writes the new tokens' k (rotated) and v into their cache
  * rows and, unless q is NULL, the rotated queries into q_out.  A token's rotary

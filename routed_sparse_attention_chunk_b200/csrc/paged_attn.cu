@@ -60,7 +60,8 @@ struct F32Smem {
   float V[kKeys][DH + 4];
   float P[8][16][kPerWarp + 8];
   float2 ml[kParts][RB];   // row maxima and sums of the parts
-  int64_t row[2][kKeys];   // element offset of each key of this tile and the next in its tensor, -1: no key
+  int64_t row[2][kKeys];   // element offset of each key of this tile and the next in its tensor, -1: no key,
+                           // -2: a page outside the pool, read as zeros
   Start st;
   static_assert(kParts * RB * DH <= kKeys * (DH + 4), "the outputs of the parts");
 };
@@ -104,7 +105,7 @@ paged_f32_kernel(PagedAttnArgs a, int TB, Mark* marks, float* slots) {
       const int64_t pg = __ldg(p.table + w.b * p.max_pages + pi);
       if (pg >= 0 && pg < p.num_pages) return pg * a.page_stride + (at - pi * p.page) * a.row_stride + w.g * a.head_stride;
       raise_flag(p.err_flag, MSA_FLAG_INDEX_OOB);
-      return -1;
+      return -2;
     };
     // Tile t of K or V; keys that do not exist are zeros.
     auto copy = [&](float (*dst)[DH + 4], const void* local, const void* bank, int t) {
@@ -192,7 +193,7 @@ paged_f32_kernel(PagedAttnArgs a, int TB, Mark* marks, float* slots) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int k = st * 32 + tx + 8 * i;
-            const bool have = sm.row[buf][k0 + k] >= 0;
+            const bool have = sm.row[buf][k0 + k] != -1;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const bool sees = have && (mem || key0 + k <= pos[j]);
@@ -498,7 +499,7 @@ __global__ void __launch_bounds__(kF32Threads, 1) paged_f32_rows_kernel(PagedAtt
   for (WalkT<true> w(sp, &sm.st); w.more(); w.next(p, sp)) {
     const Seq& s = w.s;
     const int rows = s.nq * G, pos0 = s.len - s.nq;  // rows that exist, position of the first new token
-    // element offset of one key of a tile in its tensor, -1: no key
+    // element offset of one key of a tile in its tensor, -1: no key, -2: zeros
     auto locate = [&](int t) -> int64_t {
       if (t < s.nm) {
         const int sg = t * kTileSegs + tid / kSegRows, x = tid % kSegRows;
@@ -512,7 +513,7 @@ __global__ void __launch_bounds__(kF32Threads, 1) paged_f32_rows_kernel(PagedAtt
       const int64_t pg = __ldg(p.table + w.b * p.max_pages + pi);
       if (pg >= 0 && pg < p.num_pages) return pg * a.page_stride + (at - pi * p.page) * a.row_stride + w.g * a.head_stride;
       raise_flag(p.err_flag, MSA_FLAG_INDEX_OOB);
-      return -1;
+      return -2;
     };
     __syncthreads();  // the previous segment's readers are done
     for (int e = tid; e < 16 * (DH / 4); e += kF32Threads) {
@@ -549,7 +550,7 @@ __global__ void __launch_bounds__(kF32Threads, 1) paged_f32_rows_kernel(PagedAtt
         for (int n = 0; n < kAhead; ++n) {
           const int k = k0 + n * 4 + grp;
           off[n] = sm.row[buf][k];
-          all = all && off[n] >= 0 && (mem || base + k <= pos0);
+          all = all && off[n] != -1 && (mem || base + k <= pos0);
 #pragma unroll
           for (int i = 0; i < kVec; ++i) {
             kv[n][i] = vv[n][i] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -577,7 +578,7 @@ __global__ void __launch_bounds__(kF32Threads, 1) paged_f32_rows_kernel(PagedAtt
           for (int n = 0; n < kAhead; ++n) {
 #pragma unroll
             for (int x = 4; x > 0; x >>= 1) sc[n] += __shfl_xor_sync(0xffffffffu, sc[n], x);
-            if (!all && !(off[n] >= 0 && (mem ? r0 + r < rows : base + k0 + n * 4 + grp <= last[r]))) sc[n] = minf;
+            if (!all && !(off[n] != -1 && (mem ? r0 + r < rows : base + k0 + n * 4 + grp <= last[r]))) sc[n] = minf;
             top = fmaxf(top, sc[n]);
           }
           const float corr = m[r] == minf ? 0.f : exp2f((m[r] - top) * sl2);
