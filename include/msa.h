@@ -606,8 +606,9 @@ msa_status msa_rope_backward(msa_dtype dt, const void* dout, int64_t dout_tok_st
  *            in elements (multiples of 16 bytes).  q_out may be q itself.
  *   The pages written must not be shared by sequences of the call, and k, v and
  *   q must not lie in them.  Appending the same tokens again writes the same.
- * A token whose page, position or offsets are out of range is skipped and
- * flagged (a token before position 0 raises MSA_FLAG_OFFSETS).
+ * A token whose page or position is out of range, or whose sequence's offsets are,
+ * is skipped and flagged (a token before position 0 raises MSA_FLAG_OFFSETS).
+ * Where offsets decrease, a row that several sequences claim goes to one of them.
  * ---------------------------------------------------------------------- */
 msa_status msa_paged_append(msa_dtype dt, const void* q, int64_t q_tok_stride, void* q_out, int64_t q_out_tok_stride,
                             int Hq, const void* k, int64_t k_tok_stride, const void* v, int64_t v_tok_stride,

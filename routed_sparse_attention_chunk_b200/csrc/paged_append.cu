@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(kRopeThreads) paged_append_kernel(PagedAppendA
   const int64_t q0 = __ldg(p.q_off + lo), q1 = __ldg(p.q_off + lo + 1);
   if (n < q0 || n >= q1) return;  // a row outside every sequence
   const int64_t at = (int64_t)__ldg(p.seq_len + lo) - (q1 - n);  // cache position
-  if (q1 > p.N || at < 0) {
+  if (q0 < 0 || q1 > p.N || at < 0) {
     if (report) raise_flag(p.err_flag, MSA_FLAG_OFFSETS);
     return;
   }

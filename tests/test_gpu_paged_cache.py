@@ -38,3 +38,33 @@ def test_pages_outside_the_pool_read_as_zeros(dtype, q_len, total, Hq, Hkv, d, p
         O, lse, flag = b.run(max_q=max_q)
         assert _flag(flag) == msa.FLAG_INDEX_OOB
         b.check(O, lse)
+
+
+def _append_changes(b, k, q_off):
+    """Which new tokens' cache rows an append with these offsets changed, and the flag."""
+    K0 = b.K.clone()
+    flag = torch.zeros(1, dtype=torch.int32, device=DEV)
+    msa.paged_append(None, k, k, q_off, b.seq_len, b.table, b.K, b.V, err_flag=flag)
+    changed = ~((b.K == K0) | (b.K.isnan() & K0.isnan())).flatten(2).all(2)
+    b.K.copy_(K0)
+    return _flag(flag), changed
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_append_skips_tokens_of_bad_offsets(dtype):
+    """A token whose sequence's offsets leave [0, N] is not written, at either end."""
+    b = Batch([2, 1, 3], [20, 5, 40], 4, 2, 64, 16, dtype, DEV, seed=65)
+    k = b.rnd(b.N, 2, 64) + 3.0
+    rows = lambda i: [tuple(int(x) for x in s) for s in zip(*b.slots(i, torch.arange(b.total[i] - b.q_len[i], b.total[i])))]  # noqa: E731
+    flag, changed = _append_changes(b, k, b.q_off)
+    assert flag == 0 and sorted(map(tuple, changed.nonzero().tolist())) == sorted(rows(0) + rows(1) + rows(2))
+    for first in (-1, -2 ** 40):
+        o = b.q_off.clone()
+        o[0] = first
+        flag, changed = _append_changes(b, k, o)
+        assert flag == msa.FLAG_OFFSETS and sorted(map(tuple, changed.nonzero().tolist())) == sorted(rows(1) + rows(2))
+    for last in (b.N + 1, 2 ** 40):
+        o = b.q_off.clone()
+        o[3] = last
+        flag, changed = _append_changes(b, k, o)
+        assert flag == msa.FLAG_OFFSETS and sorted(map(tuple, changed.nonzero().tolist())) == sorted(rows(0) + rows(1))
