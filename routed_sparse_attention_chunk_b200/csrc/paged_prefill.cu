@@ -346,7 +346,7 @@ paged_prefill_kernel(const __grid_constant__ TileMaps maps, PreParams a) {
       // local keys [0, seen) are visible to this row (rows that do not exist follow the last one)
       const int seen = w.s.len - w.s.nq + (rvalid ? t : min(w.i * TB + TB, w.s.nq) - 1) + 1;
       // the owner of the item's last tile sees to the next item's Q
-      const bool next_q = ((g0 + n - 1) & 1) == (uint32_t)wg && w.f + n < w.f1;
+      const bool next_q = ((g0 + n - 1) & 1) == (uint32_t)wg && w.another(sp);
       const int first = w.s.len - w.s.nq + w.i * TB;  // position of the block's first token
       const int j0 = (int)((g0 ^ wg) & 1);
       float m = -INFINITY, l_run = 0.f;  // this warpgroup's reference maximum (a whole number) and row sum

@@ -258,6 +258,10 @@ struct WalkT {
   }
   __device__ __forceinline__ bool more() const { return f < f1; }
   __device__ __forceinline__ bool whole() const { return n == T; }
+  // Whether next() will find a segment: the share goes on past this segment and the next item's start.
+  __device__ __forceinline__ bool another(const Split& sp) const {
+    return f + n + sp.cost + max(0, sp.cost - o) < f1;
+  }
   // Call only while more(); afterwards the item fields hold the next segment if more().
   __device__ __forceinline__ void next(const PagedBatch& p, const Split& sp) {
     f += sp.cost + T - o;
