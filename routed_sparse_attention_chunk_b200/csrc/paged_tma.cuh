@@ -146,11 +146,11 @@ __device__ __forceinline__ bool row_not_finite(uint8_t* tile, int r) {
   }
   return (top & 0x80008000u) != 0;
 }
-// Values of the row that are not finite become 0.  Rolled, and in few instructions: a rare path inside
-// the tile loops, which run slower the more code lies in them (23 requests with heads of 64: 119 us
-// without it, 120.6 with this, 130 unrolled by four).
+// Values of the row that are not finite become 0.  A call, not inlined: a rare path inside the tile
+// loops, which run slower the more code lies in them (23 requests with heads of 64: 119 us without
+// it, 120.6 with the call, 122.8 inlined and rolled, 130 unrolled by four).
 template <int DH>
-__device__ __forceinline__ void drop_not_finite(uint8_t* tile, int r) {
+__device__ __noinline__ void drop_not_finite(uint8_t* tile, int r) {
   uint8_t* v = tile_row<DH>(tile, r);
 #pragma unroll 1
   for (int c = 0; c < 32 * Tile<DH>::kBlocks; ++c) {
