@@ -5,7 +5,7 @@ import torch
 
 import routed_sparse_attention_chunk_b200 as msa
 
-from .paged_helpers import Batch
+from .paged_helpers import Batch, rotate64, rotation_bound
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -68,3 +68,114 @@ def test_append_skips_tokens_of_bad_offsets(dtype):
         o[3] = last
         flag, changed = _append_changes(b, k, o)
         assert flag == msa.FLAG_OFFSETS and sorted(map(tuple, changed.nonzero().tolist())) == sorted(rows(0) + rows(1))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("layout", ["kv_per_head", "kv_per_row", "padded_heads"])
+@pytest.mark.parametrize("page", [8, 16, 256])
+@pytest.mark.parametrize("d", [64, 128])
+def test_other_strides(dtype, layout, page, d):
+    """K beside V within each head, within each row, and heads apart from one another."""
+    for q_len in ([1, 1, 2], [60, 1, 5]):
+        b = Batch(q_len, [300, 131, 90], 8, 2, d, page, dtype, DEV, seed=62)
+        shape = {"kv_per_head": (b.P, page, 2, 2, d), "kv_per_row": (b.P, page, 2, 2, d),
+                 "padded_heads": (2, b.P, page, 2, d + 16)}[layout]
+        pool = torch.full(shape, float("nan"), dtype=dtype, device=DEV)
+        if layout == "kv_per_head":
+            K, V = pool[:, :, :, 0], pool[:, :, :, 1]
+        elif layout == "kv_per_row":
+            K, V = pool[:, :, 0], pool[:, :, 1]
+        else:
+            K, V = pool[0][..., :d], pool[1][..., :d]
+        K.copy_(b.K)
+        V.copy_(b.V)
+        b.K, b.V = K, V
+        O, lse, flag = b.run()
+        assert _flag(flag) == 0
+        b.check(O, lse)
+        # and the append into it: the same rows as into a dense cache, nothing beside them
+        k, v = b.rnd(b.rows, 2, d), b.rnd(b.rows, 2, d)
+        Kd, Vd = K.clone(memory_format=torch.contiguous_format), V.clone(memory_format=torch.contiguous_format)
+        before = pool.clone()
+        msa.paged_append(None, k, v, b.q_off, b.seq_len, b.table, K, V, err_flag=flag)
+        msa.paged_append(None, k, v, b.q_off, b.seq_len, b.table, Kd, Vd, err_flag=flag)
+        assert _flag(flag) == 0
+        same = lambda x, y: bool(((x == y) | (x.isnan() & y.isnan())).all())  # noqa: E731
+        assert same(K, Kd) and same(V, Vd)
+        if layout == "padded_heads":
+            assert pool[..., d:].isnan().all()
+        for i, n in enumerate(q_len):
+            pg, row = b.slots(i, torch.arange(b.total[i] - n))
+            K2 = before[:, :, :, 0] if layout == "kv_per_head" else before[:, :, 0] if layout == "kv_per_row" else before[0][..., :d]
+            assert torch.equal(K[pg, row], K2[pg, row])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("q_len,total,d", [([1, 2], [64, 64], 128), ([40, 30], [128, 128], 128), ([3, 40], [48, 48], 64)])
+def test_length_past_the_table_reads_the_table(dtype, q_len, total, d):
+    """A length past max_pages * page is that length: the same bits, and a flag."""
+    b = Batch(q_len, total, 8, 2, d, 16, dtype, DEV, seed=63)
+    b.table = b.table[:, :total[0] // 16].contiguous()
+    O1, lse1, flag = b.run()
+    assert _flag(flag) == 0
+    b.check(O1, lse1)
+    b.seq_len[1] = total[1] + 1000
+    O2, lse2, flag = b.run()
+    assert _flag(flag) == msa.FLAG_INDEX_OOB
+    assert torch.equal(O1, O2) and torch.equal(lse1, lse2)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("q_len,end,max_q", [([1, 1, 2, 1], 3, 4), ([40, 32, 60, 5], 92, 100)])
+def test_decreasing_offsets_skip_their_sequence(dtype, q_len, end, max_q):
+    """A sequence that ends before it begins is skipped; rows that only one other sequence claims hold."""
+    b = Batch(q_len, [300, 129, 200, 90], 8, 2, 128, 16, dtype, DEV, seed=64)
+    O1, lse1, _ = b.run(max_q=max_q)
+    b.q_off[1] = end  # the first sequence takes the second's rows and some of the third's
+    O2, lse2, flag = b.run(max_q=max_q)
+    assert _flag(flag) == msa.FLAG_OFFSETS
+    alone = slice(end, b.N)
+    assert torch.equal(O1[alone], O2[alone]) and torch.equal(lse1[:, alone], lse2[:, alone])
+
+
+def test_gradient_of_a_broadcast_input():
+    """One head's row read for all heads: the rows' gradients, summed over the heads, are its own."""
+    N, H, d = 20, 4, 64
+    g = torch.Generator(device=DEV).manual_seed(66)
+    one, w, u = (torch.randn(N, h, d, generator=g, device=DEV) for h in (1, H, 1))
+    cs, pos = msa.rope_table_scaled("none", 1e6, d, 32).to(DEV), torch.arange(N, dtype=torch.int32, device=DEV)
+    y, dx = torch.empty((N, H, d), device=DEV), torch.empty((N, H, d), device=DEV)
+    msa.rope_backward(w, pos, cs, dx)
+    rows = cs[pos.long()]
+    assert ((dx.double() - rotate64(w, rows, transpose=True)).abs() <= rotation_bound(w, rows, F32)).all()
+    # <w, rope(one + u / 4) - rope(one - u / 4)> 2 = <sum over heads of dx, u>: rounding as in a
+    # difference of four roundings of |one| + |u| / 4 per term, times 2 |w|
+    outs = []
+    for x in (one + 0.25 * u, one - 0.25 * u):
+        msa.rope(x.expand(N, H, d), pos, cs, y)
+        outs.append(y.double())
+    num = ((outs[0] - outs[1]) * 2 * w.double()).sum()
+    ana = (dx.double().sum(1, keepdim=True) * u.double()).sum()
+    scale = float(((one.abs() + u.abs()) * w.abs()).double().sum())
+    assert abs(float(num - ana)) <= 32 * 2.0 ** -24 * scale
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("max_q", [4, 90])
+def test_a_token_alone_and_in_a_batch(dtype, max_q):
+    """The batch decides where a sequence's keys are cut and which kernel runs, so fp32 sums change
+    their order and bf16 weights the reference they are rounded against; nothing else."""
+    b = Batch([1, 3, 2, 1], [5000, 300, 20000, 40], 8, 2, 128, 16, dtype, DEV, seed=67)
+    O1, lse1, _ = b.run(max_q=max_q)
+    want, lo, A = b.attention64()
+    bo, bl = b.bounds(want, A, lo, max(b.total))
+    for i in range(4):
+        one = Batch([1], [1], 8, 2, 128, 16, dtype, DEV, seed=1)
+        sl = slice(b.off[i], b.off[i + 1])
+        one.__dict__.update(q_len=[b.q_len[i]], total=[b.total[i]], N=b.q_len[i], rows=b.q_len[i], max_q=b.q_len[i],
+                            Q=b.Q[sl].contiguous(), q_off=b.q_off[i:i + 2] - b.q_off[i], table=b.table[i:i + 1].contiguous(),
+                            seq_len=b.seq_len[i:i + 1].contiguous(), K=b.K, V=b.V)
+        O2, lse2, flag = one.run()
+        assert _flag(flag) == 0
+        assert ((O1[sl].double() - O2.double()).abs() <= 2 * bo[sl]).all()
+        assert ((lse1[:, sl].double() - lse2.double()).abs() <= 2 * bl[:, sl]).all()
