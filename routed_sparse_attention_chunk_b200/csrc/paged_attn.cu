@@ -7,7 +7,7 @@
 //
 // The fp32 kernels are a single pass over the keys with running row maxima and sums:
 // blocks of 32 or 64 query rows over tiles of keys in shared memory
-// (paged_f32_kernel), and up to 16 rows per KV head with the keys streamed through
+// (paged_f32_kernel), and up to d / 16 rows per KV head with the keys streamed through
 // registers (paged_f32_rows_kernel).  All arithmetic is fp32 FMA; scores are compared and subtracted unscaled, so the
 // exponent's argument (s - max) * scale carries only its own rounding.
 #include <math.h>
@@ -32,6 +32,7 @@ using namespace sm100;
 
 constexpr int kF32Threads = 256;
 constexpr int kF32ItemCost = 1, kF32Slack = 2;  // see Split
+constexpr int kF32FewRows = 8;  // rows of a partial result of paged_f32_rows_kernel
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src, bool have) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(have ? 16 : 0)
@@ -461,30 +462,31 @@ __global__ void __launch_bounds__(kMergeThreads, 4) merge_kernel(const __grid_co
                        (int64_t)gridDim.x * gridDim.y * (kMergeThreads / 32));
 }
 
-// fp32 for up to 16 rows per KV head, bound by HBM: 256 threads stream the tiles' rows straight
-// into registers.  Eight lanes share a key (DH / 8 dimensions each), so a warp takes four keys at
-// once, kAhead times; every group of eight lanes keeps running maxima, sums and outputs of its own
-// for RW rows, merged within the CTA at the segment's end.  With 16 rows (kHalves = 2) half of the
-// warps take rows 0..7, half 8..15.
-template <int DH, int RW, int kHalves>
+// fp32 for RW rows per KV head: 256 threads stream the tiles' rows straight into registers.  Eight
+// lanes share a key (DH / 8 dimensions each), so a warp takes four keys at once, kAhead times; every
+// group of eight lanes keeps running maxima, sums and outputs of its own for the RW rows, merged
+// within the CTA at the segment's end.  At 4 rows 0.75 of the copy rate (64 requests of 4,096 keys,
+// heads of 128: 434 us), at 8 rows 831 us: twice the rows, twice the time, so the rows' arithmetic and
+// its shuffles bound it, with the loads' latency uncovered beside them (a warp asks for its next keys
+// when the last ones are used up).
+template <int DH, int RW>
 struct RowsSmem {
-  static constexpr int kWarps = 8 / kHalves;  // warps that share the keys of a tile
-  float Q[16][DH];
+  static constexpr int kWarps = 8;  // share the keys of a tile
+  float Q[RW][DH];
   float part[8][RW][DH];
   float2 ml[8][RW];
   int64_t row[2][kKeys];  // as in F32Smem
   Start st;
 };
 
-template <int DH, int RW, int kHalves>
+template <int DH, int RW>
 __global__ void __launch_bounds__(kF32Threads, 1) paged_f32_rows_kernel(PagedAttnArgs a, Mark* marks, float* slots) {
-  using S = RowsSmem<DH, RW, kHalves>;
+  using S = RowsSmem<DH, RW>;
   constexpr int kVec = DH / 32, kAhead = RW == 4 ? 4 : 2, kPerWarp = kKeys / S::kWarps;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   S& sm = *reinterpret_cast<S*>(smem_raw);
   const PagedBatch& p = a.p;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, grp = lane >> 3, sub = lane & 7;
-  const int kw = warp % S::kWarps, r0 = warp / S::kWarps * RW;  // this warp's keys and rows
   const int G = a.Hq / p.Hkv;
   const Split sp{p.max_q, kF32ItemCost, kF32Slack};
   pdl_wait();
@@ -516,7 +518,7 @@ __global__ void __launch_bounds__(kF32Threads, 1) paged_f32_rows_kernel(PagedAtt
       return -2;
     };
     __syncthreads();  // the previous segment's readers are done
-    for (int e = tid; e < 16 * (DH / 4); e += kF32Threads) {
+    for (int e = tid; e < RW * (DH / 4); e += kF32Threads) {
       const int r = e / (DH / 4), c = (e - r * (DH / 4)) * 4, t = r / G;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (t < s.nq) v = __ldg(reinterpret_cast<const float4*>(Q + (s.q0 + t) * a.q_ts + (w.g * G + r % G) * DH + c));
@@ -529,7 +531,7 @@ __global__ void __launch_bounds__(kF32Threads, 1) paged_f32_rows_kernel(PagedAtt
     for (int r = 0; r < RW; ++r) {
       m[r] = minf;
       l[r] = 0.f;
-      last[r] = r0 + r < rows ? pos0 + (r0 + r) / G : -1;
+      last[r] = r < rows ? pos0 + r / G : -1;
 #pragma unroll
       for (int c = 0; c < 4 * kVec; ++c) o[r][c] = 0.f;
     }
@@ -542,7 +544,7 @@ __global__ void __launch_bounds__(kF32Threads, 1) paged_f32_rows_kernel(PagedAtt
       const float* Vs = reinterpret_cast<const float*>(mem ? a.Vbar : a.V) + sub * 4;
       const int base = mem ? 0 : (t - s.nm) * kKeys;
 #pragma unroll 1
-      for (int k0 = kw * kPerWarp; k0 < (kw + 1) * kPerWarp; k0 += 4 * kAhead) {
+      for (int k0 = warp * kPerWarp; k0 < (warp + 1) * kPerWarp; k0 += 4 * kAhead) {
         int64_t off[kAhead];
         float4 kv[kAhead][kVec], vv[kAhead][kVec];
         bool all = true;  // every row of the warp sees every key of the step
@@ -568,7 +570,7 @@ __global__ void __launch_bounds__(kF32Threads, 1) paged_f32_rows_kernel(PagedAtt
           for (int n = 0; n < kAhead; ++n) sc[n] = 0.f;
 #pragma unroll
           for (int i = 0; i < kVec; ++i) {
-            const float4 q = *reinterpret_cast<const float4*>(&sm.Q[r0 + r][sub * 4 + i * 32]);
+            const float4 q = *reinterpret_cast<const float4*>(&sm.Q[r][sub * 4 + i * 32]);
 #pragma unroll
             for (int n = 0; n < kAhead; ++n)
               sc[n] = fmaf(q.x, kv[n][i].x, fmaf(q.y, kv[n][i].y, fmaf(q.z, kv[n][i].z, fmaf(q.w, kv[n][i].w, sc[n]))));
@@ -578,7 +580,7 @@ __global__ void __launch_bounds__(kF32Threads, 1) paged_f32_rows_kernel(PagedAtt
           for (int n = 0; n < kAhead; ++n) {
 #pragma unroll
             for (int x = 4; x > 0; x >>= 1) sc[n] += __shfl_xor_sync(0xffffffffu, sc[n], x);
-            if (!all && !(off[n] != -1 && (mem ? r0 + r < rows : base + k0 + n * 4 + grp <= last[r]))) sc[n] = minf;
+            if (!all && !(off[n] != -1 && (mem ? r < rows : base + k0 + n * 4 + grp <= last[r]))) sc[n] = minf;
             top = fmaxf(top, sc[n]);
           }
           const float corr = m[r] == minf ? 0.f : exp2f((m[r] - top) * sl2);
@@ -629,19 +631,19 @@ __global__ void __launch_bounds__(kF32Threads, 1) paged_f32_rows_kernel(PagedAtt
     }
     __syncthreads();
     const bool whole = w.whole();
-    float* slot = slots + slot_of(blockIdx.x, w.f, sm.st.f0) * slot_floats(16, DH);
+    float* slot = slots + slot_of(blockIdx.x, w.f, sm.st.f0) * slot_floats(kF32FewRows, DH);
     for (int e = tid; e < rows * (DH / 4); e += kF32Threads) {
-      const int r = e / (DH / 4), c = (e - r * (DH / 4)) * 4, w0 = r / RW * S::kWarps;
+      const int r = e / (DH / 4), c = (e - r * (DH / 4)) * 4;
       float top = minf, sum = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int x = 0; x < S::kWarps; ++x) top = fmaxf(top, sm.ml[w0 + x][r % RW].x);
+      for (int x = 0; x < S::kWarps; ++x) top = fmaxf(top, sm.ml[x][r].x);
 #pragma unroll
       for (int x = 0; x < S::kWarps; ++x) {
-        const float2 ml = sm.ml[w0 + x][r % RW];
+        const float2 ml = sm.ml[x][r];
         if (ml.y == 0.f) continue;
         const float f = exp2f((ml.x - top) * sl2);
-        const float4 v = *reinterpret_cast<const float4*>(&sm.part[w0 + x][r % RW][c]);
+        const float4 v = *reinterpret_cast<const float4*>(&sm.part[x][r][c]);
         sum += ml.y * f;
         acc.x = fmaf(v.x, f, acc.x);
         acc.y = fmaf(v.y, f, acc.y);
@@ -657,7 +659,7 @@ __global__ void __launch_bounds__(kF32Threads, 1) paged_f32_rows_kernel(PagedAtt
           a.lse[(int64_t)h * p.N + s.q0 + t] = sum == 0.f ? minf : top * a.scale + logf(sum);
       } else {
         *reinterpret_cast<float4*>(slot + r * DH + c) = acc;
-        if (c == 0) *reinterpret_cast<float2*>(slot + 16 * DH + 2 * r) = make_float2(top, sum);
+        if (c == 0) *reinterpret_cast<float2*>(slot + kF32FewRows * DH + 2 * r) = make_float2(top, sum);
       }
     }
   }
@@ -694,20 +696,26 @@ template <int DH>
 cudaError_t f32_blocks(const PagedAttnArgs& a, cudaStream_t s) {
   return f32_block_rows(a.Hq, a.p.Hkv, a.p.N) == 32 ? f32_block<DH, 2>(a, s) : f32_block<DH, 4>(a, s);
 }
-template <int DH, int RW, int kHalves>
-cudaError_t f32_stream(const PagedAttnArgs& a, cudaStream_t s) {
-  static std::atomic<uint64_t> done{0};
-  return f32_launch(paged_f32_rows_kernel<DH, RW, kHalves>, sizeof(RowsSmem<DH, RW, kHalves>), done,
-                    sm_count(), 16, a, s);
-}
-template <int DH>
+template <int DH, int RW>
 cudaError_t f32_few(const PagedAttnArgs& a, cudaStream_t s) {
-  const int R = a.Hq / a.p.Hkv * a.p.max_q;
-  return R <= 4 ? f32_stream<DH, 4, 1>(a, s) : R <= 8 ? f32_stream<DH, 8, 1>(a, s) : f32_stream<DH, 8, 2>(a, s);
+  static std::atomic<uint64_t> done{0};
+  return f32_launch(paged_f32_rows_kernel<DH, RW>, sizeof(RowsSmem<DH, RW>), done, sm_count(), kF32FewRows, a, s);
 }
 
-// Few rows per KV head: the kernels that hold at most 16 of them.
-bool few_rows(int Hq, int Hkv, int max_q) { return (int64_t)(Hq / Hkv) * max_q <= 16; }
+// Whether the kernels for few rows take a call, by the rows G * max_q that a sequence may have per KV
+// head.  Measured against the kernels for blocks of rows (us, few / blocks; 64 requests of 4,096 keys
+// and of 900, 16 of 1,000, one of 1,000, 4 of 30,000):
+//   bf16, heads of 128   4 rows 171/187  56/83  18/20  10/19  82/94     8 rows 177/188  62/85  20/20  11/19  84/93
+//                       12 rows 189/190  82/87  25/21  14/19  89/95    16 rows 199/189  90/86  26/21  14/19  90/94
+//   bf16, heads of 64    4 rows 136/141  42/64  17/18  11/14  56/71    16 rows 151/142  71/66  23/18  13/15  66/71
+//   fp32, heads of 128   4 rows 435/1058 126/274 42/82 12/18 201/485    8 rows 831/1101 232/285 69/85 17/18 379/504
+//                       12 rows 1607/1145 426/299 123/88 25/21 730/525
+//   fp32, heads of 64    4 rows 352/597 102/159 26/49 10/14 165/276     8 rows 673/605 187/161 47/50 14/14 308/279
+// So up to 16 rows in bf16 (few at 12 and 16 gain for one request and for long caches about what they
+// lose for some tens of short ones), in fp32 up to 8 with heads of 128 and 4 with heads of 64.
+bool few_rows(msa_dtype dt, int d, int Hq, int Hkv, int max_q) {
+  return (int64_t)(Hq / Hkv) * max_q <= (dt == MSA_F32 ? d / 16 : 16);
+}
 
 }  // namespace
 
@@ -724,20 +732,19 @@ cudaError_t launch_merge(msa_dtype dt, bool quads, const MergeArgs& m, cudaStrea
 }  // namespace paged
 
 size_t paged_attn_partial_bytes(msa_dtype dt, int Hq, int Hkv, int d, int max_q) {
-  const bool few = paged::few_rows(Hq, Hkv, max_q);
+  const bool few = paged::few_rows(dt, d, Hq, Hkv, max_q);
   // fp32 blocks: as many rows with two CTAs of 32 per SM as with one of 64
   const int grid = dt == MSA_F32 && !few ? 2 * sm_count() : sm_count();
-  const int rows = dt == MSA_F32 ? (few ? 16 : 32) : (few ? Hq / Hkv * max_q : 128);
+  const int rows = dt == MSA_F32 ? (few ? paged::kF32FewRows : 32) : (few ? Hq / Hkv * max_q : 128);
   return paged::marks_bytes(grid) + 2 * (size_t)grid * paged::slot_floats(rows, d) * sizeof(float);
 }
 
 cudaError_t launch_paged_attn(msa_dtype dt, const PagedAttnArgs& a, cudaStream_t s) {
-  const bool few = paged::few_rows(a.Hq, a.p.Hkv, a.p.max_q);
-  if (dt == MSA_F32) {
-    if (a.d == 64) return few ? paged::f32_few<64>(a, s) : paged::f32_blocks<64>(a, s);
-    return few ? paged::f32_few<128>(a, s) : paged::f32_blocks<128>(a, s);
-  }
-  return few ? launch_paged_decode(a, s) : launch_paged_prefill(a, s);
+  const bool few = paged::few_rows(dt, a.d, a.Hq, a.p.Hkv, a.p.max_q);
+  if (dt != MSA_F32) return few ? launch_paged_decode(a, s) : launch_paged_prefill(a, s);
+  if (a.d == 64) return few ? paged::f32_few<64, 4>(a, s) : paged::f32_blocks<64>(a, s);
+  if (!few) return paged::f32_blocks<128>(a, s);
+  return a.Hq / a.p.Hkv * a.p.max_q <= 4 ? paged::f32_few<128, 4>(a, s) : paged::f32_few<128, 8>(a, s);
 }
 
 }  // namespace msa

@@ -179,3 +179,14 @@ def test_a_token_alone_and_in_a_batch(dtype, max_q):
         assert _flag(flag) == 0
         assert ((O1[sl].double() - O2.double()).abs() <= 2 * bo[sl]).all()
         assert ((lse1[:, sl].double() - lse2.double()).abs() <= 2 * bl[:, sl]).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G,q", [(4, 1), (5, 1), (1, 4), (8, 1), (4, 2), (9, 1), (3, 3), (16, 1), (4, 4), (17, 1), (3, 6)])
+def test_rows_around_the_kernels_borders(dtype, d, G, q):
+    """4, 5, 8, 9, 16, 17 rows per KV head: at and beside the counts at which another kernel takes the call."""
+    b = Batch([q, 1, 0, q], [700, 40, 9, 129], 2 * G, 2, d, 32, dtype, DEV, seed=68).select(3, 9, 11, seed=8)
+    O, lse, flag = b.run(40)
+    assert _flag(flag) in (0, msa.FLAG_OVERFLOW)
+    b.check(O, lse, 40)
