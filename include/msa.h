@@ -624,8 +624,10 @@ msa_status msa_paged_append(msa_dtype dt, const void* q, int64_t q_tok_stride, v
  * sequence's selected memory rows (all visible) and cached rows [0, pos]:
  *   O = softmax(scale q K^T) V,  lse = log sum exp(scale q . k)
  * Decoding steps (n = 1), drafts, parts of prompts and mixtures of them are one
- * call; the result of a token does not depend on how the batch is put together
- * beyond the order of fp32 sums.
+ * call.  Scores, maxima, sums and partial results are fp32; in bf16 the softmax's
+ * weights are rounded to bf16 for their product with V (their sum is not).  How the
+ * batch is put together, and max_q, change a token's result by the order of fp32
+ * sums and, in bf16, by the running maximum that its weights are rounded against.
  *   Q        [N, Hq, d] dtype dt, heads d apart, token stride in elements;
  *   max_q    an upper bound of every sequence's n (a sequence above it is
  *            skipped and raises MSA_FLAG_OFFSETS); it selects the kernel
