@@ -435,9 +435,9 @@ paged_prefill_kernel(const __grid_constant__ TileMaps maps, PreParams a) {
         const float nm = m == -INFINITY ? 0.f : -m;  // no key seen yet: 2^(-inf) below is 0
         // P in registers (a pair of keys per word); the scaled arguments and the row sums in packed
         // pairs (one f32x2 instruction for two keys).  All on the transcendental unit (1,024 cycles
-        // of its time a tile): with a share of the exponentials as polynomials on the FMA pipes the
-        // 4096-token part over 32,096 keys took 2.10 ms (2 of 16 pairs) to 2.29 ms (8), without
-        // 1.97 ms.
+        // of its time a tile): a share of the exponentials as polynomials on the FMA pipes gained
+        // nothing (the 4096-token part over 32,096 keys 2.10 ms with 2 of 16 pairs, 2.29 with 8; without,
+        // 1.9 to 2.2 from run to run; 23 requests with heads of 64 130 us with 1 pair, 119 without).
         const uint64_t sl2x2 = f2_pack(sl2, sl2), nmx2 = f2_pack(nm, nm);
         uint64_t lsa2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
         uint32_t pw[kKeys / 2];
