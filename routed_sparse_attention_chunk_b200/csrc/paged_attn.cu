@@ -343,10 +343,11 @@ __device__ __forceinline__ void add_odd_to_row(const PagedAttnArgs& a, const Mar
   }
 }
 // ... and the outputs of all items that no mark names, which their CTA has written: a warp takes every
-// `warps`-th item, a lane its dimensions of a key's values.  Here, because the attention kernels run
-// slower the more code lies around their loops (23 requests with heads of 64: 120.6 us, with this at
-// each item's end 132, at the CTA's end 126), and not inlined, because the merge's registers spill
-// then (one token 11.5 us instead of 10.5).
+// `warps`-th item, a lane the sums of its dimensions over the keys so far, and a token's rows take
+// those up to its own key.  Here, because the attention kernels run slower the more code lies around
+// their loops (23 requests with heads of 64: 120.5 us, with this at each item's end 132, at the CTA's
+// end 126), and not inlined, because the merge's registers spill then (one token 11.5 us instead of
+// 10.4).
 template <int DH>
 __device__ __noinline__ void add_odd_values(const MergeArgs& ma, int64_t warp, int64_t warps) {
   constexpr int kEach = DH / 32;
@@ -366,25 +367,22 @@ __device__ __noinline__ void add_odd_values(const MergeArgs& ma, int64_t warp, i
         merged = merged || (mk.tokens > 0 && mk.b == b && mk.g == g && mk.row == s.q0 + t0);
       }
       if (__any_sync(0xffffffffu, merged)) continue;
-      const int rows = min(ma.TB, s.nq - t0) * G, first = s.len - s.nq + t0;
-      __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.O) + ((s.q0 + t0) * a.Hq + g * G) * DH;
+      const int tokens = min(ma.TB, s.nq - t0), first = s.len - s.nq + t0, from = max(1, -first);
+      float sum[kEach] = {};
 #pragma unroll 1
-      for (int key = max(first + 1, 0); key < s.len && (key - first) * G < rows; ++key) {
-        const __nv_bfloat16* v = value_row(a, b, g, key);
-        if (!v) continue;
-#pragma unroll 1
+      for (int t = from; t < tokens; ++t) {
+        const __nv_bfloat16* v = value_row(a, b, g, first + t);
+#pragma unroll
         for (int x = 0; x < kEach; ++x) {
-          const float f = __bfloat162float(v[lane * kEach + x]);
-          for (unsigned odd = __ballot_sync(0xffffffffu, !isfinite(f)); odd; odd &= odd - 1) {
-            const int from = __ffs(odd) - 1;
-            const float add = __shfl_sync(0xffffffffu, f, from);
-            for (int r = lane; r < rows; r += 32) {  // a row stays with one lane, so its sums have one order
-              if (r < (key - first) * G) continue;
-              __nv_bfloat16* dst = out + ((int64_t)(r / G) * a.Hq + r % G) * DH + from * kEach + x;
-              *dst = __float2bfloat16_rn(__bfloat162float(*dst) + add);
-            }
-          }
+          const float f = v ? __bfloat162float(v[lane * kEach + x]) : 0.f;
+          if (!isfinite(f)) sum[x] += f;
         }
+        __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(a.O) + ((s.q0 + t0 + t) * a.Hq + g * G) * DH + lane * kEach;
+#pragma unroll 1
+        for (int h = 0; h < G; ++h, dst += DH)
+#pragma unroll
+          for (int x = 0; x < kEach; ++x)
+            if (sum[x] != 0.f) dst[x] = __float2bfloat16_rn(__bfloat162float(dst[x]) + sum[x]);
       }
     }
     turn -= items;

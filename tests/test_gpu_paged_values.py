@@ -58,6 +58,26 @@ def test_values_touch_only_what_sees_them(dtype, q_len, total, Hq, Hkv, d, page)
         assert torch.equal(O2[:b.N][~odd], O1[:b.N][~odd])
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("q_len,total,Hq,Hkv,d", [
+    ([3, 1, 2], [300, 140, 77], 8, 2, 128), ([200, 30, 9], [700, 30, 300], 8, 2, 128), ([300, 40], [20000, 90], 4, 4, 64),
+    ([130, 5], [90, 5], 4, 4, 128)])
+def test_a_sequence_without_a_finite_value(dtype, q_len, total, Hq, Hkv, d):
+    """All new values of the first sequence are infinite or NaN: its tokens that see one are not finite in
+    any dimension, its lse and the other sequences keep their bits."""
+    b = Batch(q_len, total, Hq, Hkv, d, 16, dtype, DEV, seed=54)
+    O1, lse1, _ = b.run()
+    n, t = q_len[0], total[0]
+    for val in (INF, NAN):
+        pg, row = b.slots(0, torch.arange(max(t - n, 0), t))
+        b.V[pg, row] = val
+        O2, lse2, flag = b.run()
+        assert int(flag.item()) == 0 and torch.equal(lse1, lse2)
+        sees = torch.arange(n, device=DEV) + t - n >= 0
+        assert not O2[:n][sees].isfinite().any()
+        assert torch.equal(O2[n:], O1[n:]) and torch.equal(O2[:n][~sees], O1[:n][~sees])
+
+
 MINUS_INF = [
     ([3, 2], [300, 140], 128, None, 1), ([3, 2], [300, 140], 64, None, 1), ([3, 2], [300, 140], 128, 60, 1),
     ([2, 1], [700, 200], 128, None, 128), ([2, 1], [700, 200], 64, None, 128), ([2, 1], [700, 200], 128, 60, 128),
@@ -100,8 +120,9 @@ def test_fp32_keys_of_score_minus_infinity_weigh_nothing(q_len, total, d, max_q,
     _minus_infinity(F32, q_len, total, d, max_q, keys, poison)
 
 
-HARDLY = [([1], [300], 128), ([1], [300], 64), ([2], [300], 128), ([4], [300], 128), ([3], [40000], 128),
-          ([70], [300], 128), ([70], [300], 64), ([130], [9000], 128)]
+HARDLY = [(*c, where) for c in [
+    ([1], [300], 128), ([1], [300], 64), ([2], [300], 128), ([4], [300], 128), ([3], [40000], 128), ([70], [300], 128),
+    ([70], [300], 64), ([130], [9000], 128)] for where in ("first", "middle", "new", "new_low_first")[:3 + (c[0][0] > 1)]]
 
 
 def _hardly_weighs(dtype, q_len, total, d, where, val):
@@ -110,8 +131,6 @@ def _hardly_weighs(dtype, q_len, total, d, where, val):
     b = Batch(q_len, total, 8, 2, d, 16, dtype, DEV, seed=53)
     n, t = q_len[0], total[0]
     pos = {"first": 0, "middle": (t - n) // 2, "new": t - 1 - n // 3, "new_low_first": t - n}[where]
-    if where == "new_low_first" and n == 1:
-        pytest.skip("the token's own key alone")
     b.Q[:b.N] = 1.0  # the key of `pos` scores 0, all others 220 nats and more
     b.kd[0] = (b.kd[0].float().abs() + 220.0 / d ** 0.5).to(dtype)
     b.kd[0][pos] = 0
@@ -128,16 +147,14 @@ def _hardly_weighs(dtype, q_len, total, d, where, val):
     assert torch.equal(O1[:n], O2[:n])
 
 
-@pytest.mark.parametrize("q_len,total,d", HARDLY)
-@pytest.mark.parametrize("where", ["first", "middle", "new", "new_low_first"])
+@pytest.mark.parametrize("q_len,total,d,where", HARDLY)
 @pytest.mark.parametrize("val", [INF, NAN])
 def test_a_value_that_hardly_weighs_is_still_seen(q_len, total, d, where, val):
     _hardly_weighs(BF, q_len, total, d, where, val)
 
 
 
-@pytest.mark.parametrize("q_len,total,d", HARDLY)
-@pytest.mark.parametrize("where", ["first", "middle", "new", "new_low_first"])
+@pytest.mark.parametrize("q_len,total,d,where", HARDLY)
 @pytest.mark.parametrize("val", [INF, NAN])
 def test_fp32_a_value_that_hardly_weighs_is_still_seen(q_len, total, d, where, val):
     _hardly_weighs(F32, q_len, total, d, where, val)
