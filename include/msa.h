@@ -642,8 +642,9 @@ msa_status msa_paged_append(msa_dtype dt, const void* q, int64_t q_tok_stride, v
  * its K and V rows hold (NaN and infinities included): later tokens, the rest of
  * a sequence's last page, the bank rows beside a selected run.  A value that is
  * not finite makes the outputs that see it not finite in its dimension, however
- * small its weight; a key of score -inf weighs nothing, and a row that sees no
- * other key gets O = 0 and lse = -inf.
+ * small its weight; a key of score -inf weighs 0, and a row that sees no other
+ * key gets O = 0 and lse = -inf (for finite values; what the product of a weight
+ * of 0 and a value that is not finite gives is left open).
  * Supported: Hq % Hkv == 0, at most 64 query heads per KV head.  bf16 runs on the
  * tensor cores, fp32 in fp32.  The result does not depend on timing: partial sums
  * are merged in a fixed order.
